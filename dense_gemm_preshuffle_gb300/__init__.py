@@ -14,13 +14,17 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional
+from typing import NamedTuple, Optional
 
 __all__ = [
     "GP_OK", "GemmError", "DTYPES", "SCALE_MODES", "load_library", "library_path",
     "gemm_packed_b_bytes", "gemm_preshuffle_b", "gemm_unpack_b", "gemm_run",
     "gemm_last_device_status", "gemm_status_string", "gemm_debug_skip_load",
     "preshuffle_b", "matmul",
+    "ACTS", "gemm_gated_run", "gemm_gated_backward_workspace_bytes", "gemm_gated_backward", "gemm_packed_w4g_bytes",
+    "gemm_preshuffle_w4g", "gemm_unpack_w4g", "gemm_run_w4g",
+    "gated_matmul", "gated_matmul_backward", "W4Weights", "preshuffle_w4g", "unpack_w4g", "matmul_w4g",
+    "matmul_w4g_gated",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +37,7 @@ SCALE_MODES = {"none": 0, "rowcol_f32": 1, "block32_ue8m0": 2}
 GP_RUN_DEFAULT = 0
 GP_RUN_B_CONSTANT = 1
 GP_RUN_INDEPENDENT = 2
+ACTS = {"relu": 1, "silu": 2, "gelu": 3}
 EPILOGUES = {"none": 0, "bias": 1, "bias_relu": 2, "bias_silu": 3, "bias_gelu": 4}
 
 _lib = None
@@ -69,6 +74,18 @@ def load_library():
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_debug_skip_load.argtypes = [i32]
+    sz, u32 = ctypes.c_size_t, ctypes.c_uint
+    lib.gemm_gated_run.argtypes = [vp, i64, vp, i64, vp, i64, i32, i64, i64, i64, i32, vp, i64, u32, vp]
+    lib.gemm_gated_backward_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+    lib.gemm_gated_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, i64, i64, i64, i32, vp, i64, vp, i64,
+                                        vp, i64, vp, sz, vp]
+    lib.gemm_packed_w4g_bytes.argtypes = [i64, i64, i32, i32, ctypes.POINTER(sz)]
+    lib.gemm_preshuffle_w4g.argtypes = [vp, vp, vp, i64, i64, i32, vp, vp]
+    lib.gemm_unpack_w4g.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp, vp]
+    lib.gemm_run_w4g.argtypes = [vp, i64, i32, vp, vp, i32, i32, i64, i64, i64, i32, i32, vp, i64, u32, vp]
+    for name in ("gemm_gated_run", "gemm_gated_backward_workspace_bytes", "gemm_gated_backward",
+                 "gemm_packed_w4g_bytes", "gemm_preshuffle_w4g", "gemm_unpack_w4g", "gemm_run_w4g"):
+        getattr(lib, name).restype = i32
     for name in ("gemm_packed_b_bytes", "gemm_preshuffle_b", "gemm_unpack_b", "gemm_run", "gemm_run_ex",
                  "gemm_quantize_a",
                  "gemm_last_device_status", "gemm_debug_skip_load"):
@@ -184,6 +201,61 @@ def gemm_debug_skip_load(index: int) -> None:
     _check(load_library().gemm_debug_skip_load(int(index)), "gemm_debug_skip_load")
 
 
+def _act(x) -> int:
+    if isinstance(x, str):
+        if x not in ACTS:
+            raise ValueError(f"act is one of {sorted(ACTS)}: got {x!r}")
+        return ACTS[x]
+    return int(x)
+
+
+def gemm_gated_run(A, lda: int, G, ldg: int, U, ldu: int, dtype, M: int, N: int, K: int, act, H, ldh: int,
+                   flags: int = GP_RUN_DEFAULT, stream=None) -> None:
+    _check(load_library().gemm_gated_run(_ptr(A), lda, _ptr(G), ldg, _ptr(U), ldu, _dt(dtype), M, N, K, _act(act),
+                                         _ptr(H), ldh, int(flags), _stream(stream)), "gemm_gated_run")
+
+
+def gemm_gated_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gemm_gated_backward_workspace_bytes(M, N, K, ctypes.byref(out)),
+           "gemm_gated_backward_workspace_bytes")
+    return out.value
+
+
+def gemm_gated_backward(A, lda: int, G, ldg: int, U, ldu: int, dH, lddh: int, dtype, M: int, N: int, K: int, act,
+                        dA, ldda: int, dG, lddg: int, dU, lddu: int, workspace, workspace_bytes: int,
+                        stream=None) -> None:
+    _check(load_library().gemm_gated_backward(_ptr(A), lda, _ptr(G), ldg, _ptr(U), ldu, _ptr(dH), lddh, _dt(dtype),
+                                              M, N, K, _act(act), _ptr(dA), ldda, _ptr(dG), lddg, _ptr(dU), lddu,
+                                              _ptr(workspace), workspace_bytes, _stream(stream)),
+           "gemm_gated_backward")
+
+
+def gemm_packed_w4g_bytes(N: int, K: int, group: int, has_zeros: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gemm_packed_w4g_bytes(N, K, group, int(has_zeros), ctypes.byref(out)),
+           "gemm_packed_w4g_bytes")
+    return out.value
+
+
+def gemm_preshuffle_w4g(codes, scales, zeros, N: int, K: int, group: int, packed, stream=None) -> None:
+    _check(load_library().gemm_preshuffle_w4g(_ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(packed),
+                                              _stream(stream)), "gemm_preshuffle_w4g")
+
+
+def gemm_unpack_w4g(packed, N: int, K: int, group: int, has_zeros: bool, codes_out, scales_out, zeros_out,
+                    stream=None) -> None:
+    _check(load_library().gemm_unpack_w4g(_ptr(packed), N, K, group, int(has_zeros), _ptr(codes_out),
+                                          _ptr(scales_out), _ptr(zeros_out), _stream(stream)), "gemm_unpack_w4g")
+
+
+def gemm_run_w4g(A, lda: int, dtype, W_packed, U_packed, scale_dtype, has_zeros: bool, M: int, N: int, K: int,
+                 group: int, act, C, ldc: int, flags: int = GP_RUN_DEFAULT, stream=None) -> None:
+    _check(load_library().gemm_run_w4g(_ptr(A), lda, _dt(dtype), _ptr(W_packed), _ptr(U_packed), _dt(scale_dtype),
+                                       int(has_zeros), M, N, K, group, 0 if act is None else _act(act), _ptr(C), ldc,
+                                       int(flags), _stream(stream)), "gemm_run_w4g")
+
+
 # ----------------------------------------------------------------- conveniences
 
 def preshuffle_b(B, dtype, B_scales=None, stream=None):
@@ -229,3 +301,163 @@ def matmul(A, B_packed, dtype, N: int, K: int, scale_a=None, scale_b=None, out=N
                 (GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT) | (GP_RUN_INDEPENDENT if independent else 0),
                 stream)
     return out
+
+
+def _float16_type(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPES["bf16"]
+    if t.dtype == torch.float16:
+        return DTYPES["fp16"]
+    raise ValueError(f"a bf16 or fp16 tensor is wanted: got {t.dtype}")
+
+
+def _matrix(name: str, t, shape, dtype) -> int:
+    """Checks a device matrix with contiguous rows and returns its row pitch."""
+    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: a {dtype} CUDA tensor of shape {shape} is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: its rows are not contiguous (strides {t.stride()})")
+    if shape[0] <= 1 or shape[1] == 0:  # a single row's pitch is never used, nor are empty rows
+        return (max(ld, shape[1]) + 7) // 8 * 8
+    return ld
+
+
+def _new_rows(like, rows: int, cols: int):
+    """An empty [rows, cols] matrix of like's type whose rows start on 16-byte boundaries."""
+    import torch
+    ld = (cols + 7) // 8 * 8
+    t = torch.empty((rows, ld), dtype=like.dtype, device=like.device)
+    return t if ld == cols else t[:, :cols]
+
+
+def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_constant: bool = False):
+    """H = act(A W_gate^T) * (A W_up^T): the first half of a gated feed-forward block.
+
+    A [M, K], W_gate and W_up [N, K] are bf16 or fp16 device tensors, all of
+    one type, whose rows are contiguous and start on 16-byte boundaries (a
+    slice of a wider buffer will do).  act is "silu", "gelu" or "relu".
+    Returns H [M, N]; where N % 8 != 0 a new H is a slice of a wider buffer.
+    b_constant=True: no GPU work still in flight writes the weights."""
+    dt = _float16_type(A)
+    M, K = A.shape
+    N = W_gate.shape[0]
+    t = A.dtype
+    if out is None:
+        out = _new_rows(A, M, N)
+    gemm_gated_run(A, _matrix("A", A, (M, K), t), W_gate, _matrix("W_gate", W_gate, (N, K), t), W_up,
+                   _matrix("W_up", W_up, (N, K), t), dt, M, N, K, act, out, _matrix("out", out, (M, N), t),
+                   GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, stream)
+    return out
+
+
+def gated_matmul_backward(A, W_gate, W_up, dH, act: str = "silu", need_dA: bool = True, need_dW: bool = True,
+                          out=None, workspace=None, stream=None):
+    """Gradients of sum(H * dH) for H = gated_matmul(A, W_gate, W_up, act).
+
+    Returns (dA, dW_gate, dW_up) of A's type, with None for what is not
+    needed.  The inputs' products are computed again, so nothing but the
+    inputs is kept between the two passes.  out: the three tensors (or None)
+    to write into.  workspace: a uint8 device tensor of at least
+    gemm_gated_backward_workspace_bytes(M, N, K) bytes; by default one is
+    allocated for the call."""
+    import torch
+    dt = _float16_type(A)
+    M, K = A.shape
+    N = W_gate.shape[0]
+    t = A.dtype
+    dA, dG, dU = out if out is not None else (None, None, None)
+    if need_dA and dA is None:
+        dA = _new_rows(A, M, K)
+    if need_dW and dG is None:
+        dG = _new_rows(A, N, K)
+    if need_dW and dU is None:
+        dU = _new_rows(A, N, K)
+    if not need_dA:
+        dA = None
+    if not need_dW:
+        dG = dU = None
+    if workspace is None:
+        workspace = torch.empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=A.device)
+    gemm_gated_backward(A, _matrix("A", A, (M, K), t), W_gate, _matrix("W_gate", W_gate, (N, K), t), W_up,
+                        _matrix("W_up", W_up, (N, K), t), dH, _matrix("dH", dH, (M, N), t), dt, M, N, K, act,
+                        dA, 0 if dA is None else _matrix("dA", dA, (M, K), t),
+                        dG, 0 if dG is None else _matrix("dW_gate", dG, (N, K), t),
+                        dU, 0 if dU is None else _matrix("dW_up", dU, (N, K), t),
+                        workspace, workspace.numel() * workspace.element_size(), stream)
+    return dA, dG, dU
+
+
+class W4Weights(NamedTuple):
+    """4-bit weights W [N, K] packed by preshuffle_w4g, as the products take them."""
+    packed: object        # uint8 device tensor
+    N: int
+    K: int
+    group: int            # K values that share a scale
+    scale_dtype: int      # DTYPES["bf16"] or DTYPES["fp16"]
+    has_zeros: bool       # zero points of their own, else 8 throughout
+
+
+def preshuffle_w4g(codes, scales, group: int, zeros=None, stream=None) -> W4Weights:
+    """Pack W[n, k] = (code - zero) * scale, once, offline.
+
+    codes: uint8 [N, K/2] device tensor, two codes 0..15 per byte, the even-k
+    one in the low nibble.  scales: bf16 or fp16 [N, ceil(K/group)].  zeros:
+    uint8 of scales' shape with values 0..15, or None for 8 throughout.
+    group: 32, 64 or 128.  All contiguous."""
+    import torch
+    N, K = codes.shape[0], codes.shape[1] * 2
+    sd = _float16_type(scales)
+    shape = (N, (K + group - 1) // group) if group > 0 else None
+    for name, x, dtype, want in (("codes", codes, torch.uint8, (N, K // 2)), ("scales", scales, scales.dtype, shape),
+                                 ("zeros", zeros, torch.uint8, shape)):
+        if x is not None and (x.dtype != dtype or not x.is_cuda or tuple(x.shape) != want or not x.is_contiguous()):
+            raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {want} is wanted, got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+    packed = torch.empty(gemm_packed_w4g_bytes(N, K, group, zeros is not None), dtype=torch.uint8,
+                         device=codes.device)
+    gemm_preshuffle_w4g(codes, scales, zeros, N, K, group, packed, stream)
+    return W4Weights(packed, N, K, group, sd, zeros is not None)
+
+
+def unpack_w4g(W: W4Weights, stream=None):
+    """The inverse of preshuffle_w4g: (codes, scales, zeros or None)."""
+    import torch
+    dev = W.packed.device
+    groups = (W.K + W.group - 1) // W.group
+    codes = torch.empty((W.N, W.K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((W.N, groups), device=dev,
+                         dtype=torch.float16 if W.scale_dtype == DTYPES["fp16"] else torch.bfloat16)
+    zeros = torch.empty((W.N, groups), dtype=torch.uint8, device=dev) if W.has_zeros else None
+    gemm_unpack_w4g(W.packed, W.N, W.K, W.group, W.has_zeros, codes, scales, zeros, stream)
+    return codes, scales, zeros
+
+
+def _run_w4g(A, W: W4Weights, U: Optional[W4Weights], act, out, stream, b_constant: bool):
+    import torch
+    dt = _float16_type(A)
+    M = A.shape[0]
+    if out is None:
+        out = torch.empty((M, W.N), dtype=A.dtype, device=A.device)
+    lda, ldc = _matrix("A", A, (M, W.K), A.dtype), _matrix("out", out, (M, W.N), A.dtype)
+    gemm_run_w4g(A, lda, dt, W.packed, None if U is None else U.packed, W.scale_dtype, W.has_zeros, M, W.N, W.K,
+                 W.group, act, out, ldc, GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, stream)
+    return out
+
+
+def matmul_w4g(A, W: W4Weights, out=None, stream=None, b_constant: bool = False):
+    """C = A . W^T for a few rows of A [M, K] (bf16 or fp16) and packed 4-bit
+    weights; returns [M, N] of A's type.  b_constant=True: no GPU work still
+    in flight writes the packed weights (pack once, then synchronise)."""
+    return _run_w4g(A, W, None, None, out, stream, b_constant)
+
+
+def matmul_w4g_gated(A, W_gate: W4Weights, W_up: W4Weights, act: str = "silu", out=None, stream=None,
+                     b_constant: bool = False):
+    """act(A . W_gate^T) * (A . W_up^T) with both weights packed in 4 bits
+    (of one shape, group, scale type and kind of zero points)."""
+    if tuple(W_gate[1:]) != tuple(W_up[1:]):
+        raise ValueError(f"W_gate and W_up differ: {tuple(W_gate[1:])} and {tuple(W_up[1:])}")
+    return _run_w4g(A, W_gate, W_up, act, out, stream, b_constant)

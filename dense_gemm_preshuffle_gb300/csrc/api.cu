@@ -147,6 +147,24 @@ int raster_group(int64_t tiles_m, int64_t tile_rows, int64_t kbytes, int64_t l2_
 }
 
 }  // namespace
+
+int host_context(HostContext* out) {
+  DeviceInfo* d = nullptr;
+  if (const int rc = device_info(&d); rc != GP_OK) return rc;
+  out->num_sms = d->num_sms;
+  out->l2_bytes = d->l2_bytes;
+  out->status = d->status;
+  out->wait_limit_ns = wait_limit_ns();
+  return GP_OK;
+}
+
+int encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
+  return encode_2d(map, type, ptr, inner, outer, row_bytes, box_inner, box_outer, swz);
+}
+
+int take_debug_skip_load() { return g_debug_skip_load.exchange(0); }
+
 }  // namespace gp
 
 using namespace gp;

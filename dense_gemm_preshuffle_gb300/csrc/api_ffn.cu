@@ -1,0 +1,188 @@
+// C ABI of the feed-forward operators (declared in
+// include/gemm_preshuffle.h): the gated products with their gradients, and
+// the products with 4-bit group-scaled weights.  Every argument is checked
+// here, on the host, before anything is launched.
+#include "kernels.h"
+
+using namespace gp;
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool bad_dims(int64_t M, int64_t N, int64_t K) {
+  return M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim;
+}
+
+// A pitch in 16-bit elements: every row on a 16-byte boundary, and within
+// the 2^40-byte stride that a tensor map can hold.
+bool bad_pitch(int64_t ld, int64_t width) { return ld < width || ld % 8 != 0 || ld >= (int64_t(1) << 38); }
+
+bool float16_type(int dtype) { return dtype == GP_BF16 || dtype == GP_FP16; }
+
+int check_type(int dtype) {
+  if (dtype < GP_BF16 || dtype > GP_W4A8) return GP_ERR_INVALID_ARG;
+  return float16_type(dtype) ? GP_OK : GP_ERR_UNSUPPORTED;
+}
+
+bool bad_act(int act) { return act < GP_ACT_RELU || act > GP_ACT_GELU; }
+
+bool bad_flags(unsigned flags) { return (flags & ~(unsigned)(GP_RUN_B_CONSTANT | GP_RUN_INDEPENDENT)) != 0; }
+
+// An output whose rows are zeroed, `width` 16-bit elements each.
+int zero_rows(void* p, int64_t ld, int64_t width, int64_t rows, cudaStream_t st) {
+  return cudaMemset2DAsync(p, (size_t)ld * 2, 0, (size_t)width * 2, (size_t)rows, st) == cudaSuccess ? GP_OK
+                                                                                                    : GP_ERR_CUDA;
+}
+
+int check_w4g(int64_t N, int64_t K, int group, int has_zeros) {
+  if ((group != 32 && group != 64 && group != 128) || (has_zeros != 0 && has_zeros != 1)) return GP_ERR_INVALID_ARG;
+  if (bad_dims(0, N, K) || K % 32 != 0) return GP_ERR_SHAPE;
+  return GP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_gated_run(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu, int dtype,
+                   int64_t M, int64_t N, int64_t K, int act, void* H, int64_t ldh, unsigned flags, void* stream) {
+  if (bad_flags(flags) || bad_act(act)) return GP_ERR_INVALID_ARG;
+  int rc = check_type(dtype);
+  if (rc != GP_OK) return rc;
+  if (bad_dims(M, N, K) || bad_pitch(lda, K) || bad_pitch(ldg, K) || bad_pitch(ldu, K) || bad_pitch(ldh, N))
+    return GP_ERR_SHAPE;
+  if (M == 0 || N == 0) return GP_OK;
+  if (H == nullptr || (K > 0 && (A == nullptr || G == nullptr || U == nullptr))) return GP_ERR_INVALID_ARG;
+  if (!aligned16(H) || (K > 0 && (!aligned16(A) || !aligned16(G) || !aligned16(U)))) return GP_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (K == 0) return zero_rows(H, ldh, N, M, st);
+  HostContext ctx;
+  if ((rc = host_context(&ctx)) != GP_OK) return rc;
+  GatedArgs a{};
+  a.A = A, a.G = G, a.U = U, a.H = H;
+  a.lda = lda, a.ldg = ldg, a.ldu = ldu, a.ldh = ldh;
+  a.fp16 = dtype == GP_FP16;
+  a.M = M, a.N = N, a.K = K;
+  a.act = act;
+  a.b_constant = flags != 0;
+  return gated_run_launch(a, ctx, st);
+}
+
+int gemm_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes_out) {
+  if (bytes_out == nullptr) return GP_ERR_INVALID_ARG;
+  if (bad_dims(M, N, K)) return GP_ERR_SHAPE;
+  *bytes_out = (M == 0 || N == 0 || K == 0) ? 0 : gated_workspace_bytes(M, N, K);
+  return GP_OK;
+}
+
+int gemm_gated_backward(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu,
+                        const void* dH, int64_t lddh, int dtype, int64_t M, int64_t N, int64_t K, int act, void* dA,
+                        int64_t ldda, void* dG, int64_t lddg, void* dU, int64_t lddu, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (bad_act(act) || (dG == nullptr) != (dU == nullptr)) return GP_ERR_INVALID_ARG;
+  int rc = check_type(dtype);
+  if (rc != GP_OK) return rc;
+  if (bad_dims(M, N, K) || bad_pitch(lda, K) || bad_pitch(ldg, K) || bad_pitch(ldu, K) || bad_pitch(lddh, N) ||
+      (dA != nullptr && bad_pitch(ldda, K)) || (dG != nullptr && (bad_pitch(lddg, K) || bad_pitch(lddu, K))))
+    return GP_ERR_SHAPE;
+  if (K == 0 || (dA == nullptr && dG == nullptr)) return GP_OK;
+  if (!aligned16(dA) || !aligned16(dG) || !aligned16(dU)) return GP_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0 || N == 0) {  // an empty sum (or nothing at all) in each gradient
+    if (M > 0 && dA != nullptr) return zero_rows(dA, ldda, K, M, st);
+    if (N > 0 && dG != nullptr) {
+      if ((rc = zero_rows(dG, lddg, K, N, st)) != GP_OK) return rc;
+      return zero_rows(dU, lddu, K, N, st);
+    }
+    return GP_OK;
+  }
+  if (A == nullptr || G == nullptr || U == nullptr || dH == nullptr || workspace == nullptr)
+    return GP_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(G) || !aligned16(U) || !aligned16(dH) || !aligned16(workspace))
+    return GP_ERR_ALIGNMENT;
+  if (workspace_bytes < gated_workspace_bytes(M, N, K)) return GP_ERR_SHAPE;
+  HostContext ctx;
+  if ((rc = host_context(&ctx)) != GP_OK) return rc;
+  GatedArgs a{};
+  a.A = A, a.G = G, a.U = U, a.dH = dH;
+  a.lda = lda, a.ldg = ldg, a.ldu = ldu, a.lddh = lddh;
+  a.dA = dA, a.dG = dG, a.dU = dU;
+  a.ldda = ldda, a.lddg = lddg, a.lddu = lddu;
+  a.fp16 = dtype == GP_FP16;
+  a.M = M, a.N = N, a.K = K;
+  a.act = act;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return gated_backward_launch(a, ctx, st);
+}
+
+int gemm_packed_w4g_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* bytes_out) {
+  if (bytes_out == nullptr) return GP_ERR_INVALID_ARG;
+  if (const int rc = check_w4g(N, K, group, has_zeros); rc != GP_OK) return rc;
+  *bytes_out = (size_t)w4g_layout(N, K, group, has_zeros != 0).bytes;
+  return GP_OK;
+}
+
+int gemm_preshuffle_w4g(const void* codes, const void* scales, const void* zeros, int64_t N, int64_t K, int group,
+                        void* packed, void* stream) {
+  if (const int rc = check_w4g(N, K, group, zeros != nullptr); rc != GP_OK) return rc;
+  if (N == 0 || K == 0) return GP_OK;
+  if (codes == nullptr || scales == nullptr || packed == nullptr) return GP_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned16(packed)) return GP_ERR_ALIGNMENT;
+  return w4g_pack_launch(static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
+                         static_cast<const uint8_t*>(zeros), N, K, group, static_cast<uint8_t*>(packed),
+                         static_cast<cudaStream_t>(stream));
+}
+
+int gemm_unpack_w4g(const void* packed, int64_t N, int64_t K, int group, int has_zeros, void* codes_out,
+                    void* scales_out, void* zeros_out, void* stream) {
+  if (const int rc = check_w4g(N, K, group, has_zeros); rc != GP_OK) return rc;
+  if (N == 0 || K == 0) return GP_OK;
+  if (packed == nullptr || codes_out == nullptr || scales_out == nullptr ||
+      (has_zeros != 0) != (zeros_out != nullptr))
+    return GP_ERR_INVALID_ARG;
+  if (!aligned16(codes_out) || !aligned16(scales_out) || !aligned16(zeros_out) || !aligned16(packed))
+    return GP_ERR_ALIGNMENT;
+  return w4g_unpack_launch(static_cast<const uint8_t*>(packed), N, K, group, has_zeros != 0,
+                           static_cast<uint8_t*>(codes_out), static_cast<uint16_t*>(scales_out),
+                           static_cast<uint8_t*>(zeros_out), static_cast<cudaStream_t>(stream));
+}
+
+int gemm_run_w4g(const void* A, int64_t lda, int dtype, const void* W_packed, const void* U_packed, int scale_dtype,
+                 int has_zeros, int64_t M, int64_t N, int64_t K, int group, int act, void* C, int64_t ldc,
+                 unsigned flags, void* stream) {
+  if (bad_flags(flags) || (U_packed == nullptr ? act != 0 : bad_act(act))) return GP_ERR_INVALID_ARG;
+  int rc = check_type(dtype);
+  if (rc == GP_OK) rc = check_type(scale_dtype);
+  if (rc == GP_OK) rc = check_w4g(N, K, group, has_zeros);
+  if (rc != GP_OK) return rc;
+  if (M < 0 || M >= kMaxDim || bad_pitch(lda, K) || ldc < N) return GP_ERR_SHAPE;
+  if (M == 0 || N == 0) return GP_OK;
+  if (C == nullptr || (K > 0 && (A == nullptr || W_packed == nullptr))) return GP_ERR_INVALID_ARG;
+  if (!aligned16(C) || (K > 0 && (!aligned16(A) || !aligned16(W_packed) || !aligned16(U_packed))))
+    return GP_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (K == 0) return zero_rows(C, ldc, N, M, st);
+  HostContext ctx;
+  if ((rc = host_context(&ctx)) != GP_OK) return rc;
+  W4gArgs a{};
+  a.A = A;
+  a.lda = lda;
+  a.fp16 = dtype == GP_FP16;
+  a.W = static_cast<const uint8_t*>(W_packed);
+  a.U = static_cast<const uint8_t*>(U_packed);
+  a.scale_fp16 = scale_dtype == GP_FP16;
+  a.has_zeros = has_zeros != 0;
+  a.M = M, a.N = N, a.K = K;
+  a.group = group;
+  a.act = act;
+  a.C = C;
+  a.ldc = ldc;
+  a.b_constant = flags != 0;
+  return w4g_run_launch(a, ctx, st);
+}
+
+}  // extern "C"

@@ -29,6 +29,21 @@ inline int smem_attr_once(std::atomic<bool> (&done)[64], Kern kern, int bytes, i
   return GP_OK;
 }
 
+// What a launcher needs to know of the current device (api.cu).
+struct HostContext {
+  int num_sms;
+  int64_t l2_bytes;
+  uint32_t* status;        // device status word
+  uint64_t wait_limit_ns;  // bound of every in-kernel wait
+};
+int host_context(HostContext* out);
+// A 2-D tensor map over row-major data: `inner` elements a row, `outer` rows
+// `row_bytes` apart, boxes of box_inner x box_outer elements.
+int encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+// The armed index of gemm_debug_skip_load, which this call disarms.
+int take_debug_skip_load();
+
 struct TcParams {
   const uint8_t* Bp;      // packed B (data region)
   const uint8_t* Bsf;     // packed B scales (E2M1 only)
@@ -124,6 +139,51 @@ int i8_gemm_launch(const CUtensorMap& tmA, const CUtensorMap& tmB, I8Params p, i
 
 int quant_launch(const void* X, bool x_bf16, int64_t M, int64_t K, bool to_e2m1, void* Q, void* S, int num_sms,
                  uint32_t* status, uint64_t limit_ns, cudaStream_t stream);
+
+// Gated feed-forward products (gated.cu).  Arguments are as checked by the C
+// ABI: every size is at least 1.
+struct GatedArgs {
+  const void *A, *G, *U, *dH;
+  int64_t lda, ldg, ldu, lddh;
+  void *H, *dA, *dG, *dU;      // H forward; dA, dG, dU backward (each may be null)
+  int64_t ldh, ldda, lddg, lddu;
+  bool fp16;                   // element type: IEEE half, else bf16
+  int64_t M, N, K;
+  int act;                     // gp_act
+  bool b_constant;
+  void* workspace;             // backward: gated_workspace_bytes()
+  size_t workspace_bytes;
+};
+size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int gated_run_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream);
+int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream);
+
+// 4-bit weights with group scales (w4g.cu).
+struct W4gArgs {
+  const void* A;
+  int64_t lda;
+  bool fp16;                   // type of A and C
+  const uint8_t *W, *U;        // packed; U null: a plain product
+  bool scale_fp16, has_zeros;
+  int64_t M, N, K;
+  int group;
+  int act;
+  void* C;
+  int64_t ldc;
+  bool b_constant;
+};
+// Byte offsets of the scale and zero-point regions of a packed buffer, and
+// its size.
+struct W4gLayout {
+  int64_t row_tiles, kblocks;  // ceil(N / 16), ceil(K / 128)
+  int64_t scales, zeros, bytes;
+};
+W4gLayout w4g_layout(int64_t N, int64_t K, int group, bool has_zeros);
+int w4g_pack_launch(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                    int group, uint8_t* packed, cudaStream_t stream);
+int w4g_unpack_launch(const uint8_t* packed, int64_t N, int64_t K, int group, bool has_zeros, uint8_t* codes,
+                      uint16_t* scales, uint8_t* zeros, cudaStream_t stream);
+int w4g_run_launch(const W4gArgs& a, const HostContext& ctx, cudaStream_t stream);
 
 // Packed-B layouts: 128-row bands, bytes as given (tcgen05 types); 8-row
 // bands in offset binary (INT8); 8-row bands, interleaved offset-binary

@@ -26,7 +26,7 @@
  *     quantiser kernels set a sticky status word.  gemm_last_device_status()
  *     reads and clears it.
  *   - Matrices are row-major and densely packed (row pitch = K elements for
- *     A and B, N elements for C).
+ *     A and B, N elements for C), except where an entry point takes pitches.
  *   - Every device pointer must be 16-byte aligned.
  *   - Thread safety: calls from several host threads are safe.  Each call
  *     keeps its state on the stack, apart from a per-device table of SM
@@ -266,6 +266,153 @@ int gemm_last_device_status(void* stream);
  */
 int gemm_quantize_a(const void* X, int x_dtype, int64_t M, int64_t K, int q_dtype, void* A_out,
                     void* scales_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward products.
+ *
+ *   H[M,N] = act(A G^T) * (A U^T)          (element by element)
+ *
+ * for an activation A [M,K] and the two projections G (gate) and U (up),
+ * both [N,K]: the first half of a gated feed-forward block.  gemm_run is its
+ * second half (the down projection).
+ *
+ * G and U are read as they are, row-major and unpacked: a training step
+ * changes them on every call, and its gradients are laid out like them.
+ * The operands of these entry points have a row pitch of their own (ld*,
+ * in elements): any M, N, K >= 0 is accepted as long as every row starts on
+ * a 16-byte boundary, i.e. ld* % 8 == 0 and ld* >= the row's length.  What
+ * lies between a row's end and the next row has no effect and is not written.
+ * dtype is GP_BF16 or GP_FP16 for every operand of a call.  Products are
+ * accumulated in fp32, the activation and its slope are evaluated in fp32.
+ * ------------------------------------------------------------------------ */
+
+/* act(v) of the gated products: ReLU max(v, 0), with slope 0 at v <= 0; SiLU v / (1 + e^-v);
+ * GELU 0.5 v (1 + erf(v / sqrt 2)). */
+typedef enum gp_act {
+  GP_ACT_RELU = 1,
+  GP_ACT_SILU = 2,
+  GP_ACT_GELU = 3
+} gp_act;
+
+/*
+ * H = act(A G^T) * (A U^T), rounded once, to nearest even, from fp32.
+ *
+ * A : device, [M, K], pitch lda.   G, U : device, [N, K], pitches ldg, ldu.
+ * H : device, [M, N], pitch ldh, written entirely; it overlaps no input.
+ * flags : GP_RUN_B_CONSTANT (G and U are constant weights, as in
+ *         gemm_run_ex) and GP_RUN_INDEPENDENT, which is taken as
+ *         GP_RUN_B_CONSTANT here.
+ * M == 0 or N == 0 is a no-op; K == 0 writes act(0) * 0 = 0.  One kernel on
+ * `stream` (K == 0: an async memset); nothing is allocated.
+ * Errors: GP_ERR_INVALID_ARG (null pointer, unknown dtype value, act or
+ * flag), GP_ERR_UNSUPPORTED (dtype is not a 16-bit float), GP_ERR_SHAPE (a
+ * size is negative or >= 2^31, or a pitch is shorter than its row or not a
+ * multiple of 8), GP_ERR_ALIGNMENT (a pointer is not 16-byte aligned).
+ */
+int gemm_gated_run(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu, int dtype,
+                   int64_t M, int64_t N, int64_t K, int act, void* H, int64_t ldh, unsigned flags, void* stream);
+
+/*
+ * Bytes of workspace that gemm_gated_backward needs for these sizes (0 when
+ * a size is 0).  Host-only call.
+ */
+int gemm_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes_out);
+
+/*
+ * The gradients of sum(H * dH) for H = act(A G^T) * (A U^T).  With
+ * g = A G^T and u = A U^T, which are computed again from A, G and U:
+ *
+ *   dg = dH * u * act'(g)      du = dH * act(g)
+ *   dA = dg G + du U           dG = dg^T A           dU = du^T A
+ *
+ * dg and du are rounded to dtype (they are operands of the tensor cores);
+ * everything else is fp32 until each result's one rounding.
+ *
+ * dH : device, [M, N], pitch lddh.
+ * dA : device, [M, K], pitch ldda, or NULL where A needs no gradient.
+ * dG, dU : device, [N, K], pitches lddg, lddu; both NULL where the weights
+ *      need no gradient, else both given.  Outputs overlap no input.
+ * workspace : device, 16-byte aligned, of at least
+ *      gemm_gated_backward_workspace_bytes(); its contents are destroyed.
+ * Results do not depend on what the workspace or the outputs held, and are
+ * the same bits for the same inputs.  M == 0 writes zero weight gradients;
+ * N == 0 a zero dA.  Errors as gemm_gated_run; a workspace that is NULL
+ * where one is needed is GP_ERR_INVALID_ARG, one that is too small
+ * GP_ERR_SHAPE.
+ */
+int gemm_gated_backward(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu,
+                        const void* dH, int64_t lddh, int dtype, int64_t M, int64_t N, int64_t K, int act, void* dA,
+                        int64_t ldda, void* dG, int64_t lddg, void* dU, int64_t lddu, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products with 4-bit weights and group scales, for a few rows of A (single
+ * tokens to a decode batch):
+ *
+ *   C[M,N] = A[M,K] . W[N,K]^T,   W[n,k] = (q[n,k] - z[n,j]) * s[n,j],  j = k / group
+ *
+ * with codes q in 0..15, 16-bit float scales s and zero points z in 0..15
+ * (8 throughout where none are given).  A stays in 16 bits (W4A8, for int8
+ * activations and no scales, is a dtype of gemm_run).
+ * Shape rules: K % 32 == 0, group is 32, 64 or 128 (a last group may be
+ * short), any N.
+ * ------------------------------------------------------------------------ */
+
+/* Size in bytes of the packed form of W.  has_zeros: 0 or 1.  Host-only call. */
+int gemm_packed_w4g_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* bytes_out);
+
+/*
+ * The offline preshuffle of W.
+ *
+ * codes  : device, [N, K/2] bytes, row-major, two codes per byte, the
+ *          even-k code in the low nibble.
+ * scales : device, [N, ceil(K/group)] row-major, bf16 or fp16 (copied as
+ *          they are; gemm_run_w4g is told which).
+ * zeros  : device, uint8 [N, ceil(K/group)] row-major, or NULL: 8 throughout.
+ * packed : device, gemm_packed_w4g_bytes() bytes, written entirely.
+ *
+ * Layout: three regions, each cut into blocks of 16 rows x 128 K values
+ * (block (r, c) at index r * ceil(K/128) + c; codes and scales past N or K
+ * are 0):
+ *   - codes, 1024 bytes a block: the 32-bit word i (0..3) of lane 4g + t and
+ *     half h, at byte (h*32 + 4g + t)*16 + 4i, holds row 16r + 8h + g,
+ *     k0 = 128c + 32i + 8t: codes k0..k0+7 at bits 0, 16, 4, 20, 8, 24, 12, 28.
+ *   - scales: 16 * 128/group values a block, group by group; within a group
+ *     row 8h + g is at 2g + h.
+ *   - zero points, where given: bytes in the scales' order.
+ * One kernel on `stream`.
+ */
+int gemm_preshuffle_w4g(const void* codes, const void* scales, const void* zeros, int64_t N, int64_t K, int group,
+                        void* packed, void* stream);
+
+/* The inverse of gemm_preshuffle_w4g, for round-trip checks.  zeros_out is
+ * required when has_zeros is 1 and NULL otherwise. */
+int gemm_unpack_w4g(const void* packed, int64_t N, int64_t K, int group, int has_zeros, void* codes_out,
+                    void* scales_out, void* zeros_out, void* stream);
+
+/*
+ * C = A . W^T, or, with a second packed matrix U of the same shape, group,
+ * scale type and zero points, C = act(A . W^T) * (A . U^T).
+ *
+ * A         : device, [M, K], pitch lda (lda % 8 == 0), dtype GP_BF16 or GP_FP16.
+ * W_packed  : device, output of gemm_preshuffle_w4g for N, K, group.
+ * U_packed  : NULL, or a second one; `act` is then a gp_act, and 0 with NULL.
+ * scale_dtype : GP_BF16 or GP_FP16, the type of the packed scales.
+ * C         : device, [M, N], pitch ldc >= N (any), of A's dtype, written entirely.
+ * flags     : GP_RUN_B_CONSTANT: the packed weights may be read before the
+ *             preceding kernel on `stream` has finished; GP_RUN_INDEPENDENT is
+ *             taken as that.
+ * Codes enter the products exactly; sums are fp32; one rounding at the end.
+ * The weights are read once per 32 rows of A, so this is for small M; any
+ * M < 2^31 is accepted.  Finite A is expected (|A| < 2^100 for bf16): rows
+ * with infinities or NaN give infinities or NaN.  Results are the same bits
+ * for the same inputs.  One kernel on `stream`; nothing is allocated.
+ * M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Errors as
+ * gemm_gated_run; a bad group or has_zeros is GP_ERR_INVALID_ARG.
+ */
+int gemm_run_w4g(const void* A, int64_t lda, int dtype, const void* W_packed, const void* U_packed, int scale_dtype,
+                 int has_zeros, int64_t M, int64_t N, int64_t K, int group, int act, void* C, int64_t ldc,
+                 unsigned flags, void* stream);
 
 /* Static, human-readable name of a gp_status value. */
 const char* gemm_status_string(int status);
