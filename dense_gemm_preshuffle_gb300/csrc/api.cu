@@ -163,6 +163,18 @@ int encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, u
   return encode_2d(map, type, ptr, inner, outer, row_bytes, box_inner, box_outer, swz);
 }
 
+int encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t slices, uint64_t row_bytes, uint64_t slice_bytes, uint32_t box_inner, uint32_t box_outer,
+                  uint32_t box_slices, CUtensorMapSwizzle swz) {
+  cuuint64_t dims[3] = {inner, outer, slices};
+  cuuint64_t strides[2] = {row_bytes, slice_bytes};
+  cuuint32_t box[3] = {box_inner, box_outer, box_slices};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GP_OK : GP_ERR_CUDA;
+}
+
 int take_debug_skip_load() { return g_debug_skip_load.exchange(0); }
 
 }  // namespace gp

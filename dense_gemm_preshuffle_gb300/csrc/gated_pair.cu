@@ -1,0 +1,575 @@
+// Tensor-core products of the gated feed-forward block: pairs of CTAs
+// (tcgen05 cta_group::2), 16-bit operands straight from the caller's
+// row-major matrices, fp32 accumulators in tensor memory.
+//
+//   FORWARD  H  = act(A G^T) * (A U^T)
+//   SLOPES   dg = dH (A U^T) act'(A G^T),  du = dH act(A G^T)
+//   INPUT    dA = dg G + du U              (one sum over both halves)
+//   WEIGHTS  dG = dg^T A,  dU = du^T A     (one launch over both)
+//
+// A 2-CTA cluster computes a 256-row tile whose MMAs are M = 256, N = 256,
+// K = 16; CTA r holds 128 of A's rows and 128 of B's.  The reduction advances
+// 64 values (one ring stage, 32 KiB a CTA) at a time.
+//   - FORWARD and SLOPES tile 256 tokens x 128 columns of H.  CTA 0 loads the
+//     128 rows of G and CTA 1 the same rows of U, so that one MMA makes both
+//     products: every CTA finds g in accumulator columns 0-127 and u in
+//     128-255 of its own tokens, and the gate needs no exchange.
+//   - INPUT and WEIGHTS reduce over a dimension that is not contiguous in
+//     memory (weights by rows of G and U, activations by tokens).  Those
+//     operands are MN-major: a TMA box of 64 contiguous values x 64 reduction
+//     steps lands in the swizzled MN-major layout, and the MMA transposes as
+//     it reads.  Nothing is transposed in memory.
+//   - Sizes that tiles do not divide: TMA reads zeros past the matrix and
+//     clips its stores, so ragged tiles take the same path.  A TMA store's
+//     clip is a whole 16-byte unit, so the caller's outputs are mapped up to
+//     their last multiple of 8 columns and the few columns after it are
+//     written from registers: what lies behind a row's end stays as it was.
+// Two accumulators (512 TMEM columns) let each tile's epilogue run beside the
+// next tile's MMAs.  A product of few tiles and a long reduction is split
+// along it (INPUT, WEIGHTS): each part writes fp32 sums to the workspace and
+// a second kernel adds them in order, so results do not depend on timing.
+//
+// Roles as in gemm_pair.cu: warp 0 copies (lane 0 B, lane 1 A), warp 1 issues
+// the MMAs in the even CTA, warps 2-9 are the epilogue, two for each TMEM
+// lane quarter.  Every wait is bounded.
+#include <cuda_fp16.h>
+
+#include "gated_math.cuh"
+#include "gated_pair.h"
+#include "ptx.cuh"
+
+namespace gp {
+
+namespace {
+
+constexpr int GP_EPI_WARPS = 8;
+constexpr int GP_THREADS = 32 * (2 + GP_EPI_WARPS);
+constexpr int OPERAND_BYTES = 128 * 128;  // one operand of one stage of one CTA
+constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
+constexpr int MN_BLOCK_BYTES = 64 * 128;  // 64 values x 64 reduction steps
+
+template <int MODE>
+struct Cfg {
+  static constexpr bool kGate = MODE == GATED_FORWARD || MODE == GATED_SLOPES;  // two products a tile
+  static constexpr bool kAMn = MODE == GATED_WEIGHTS;
+  static constexpr bool kBMn = MODE == GATED_INPUT || MODE == GATED_WEIGHTS;
+  static constexpr int kStaging = MODE == GATED_SLOPES ? 2 : 1;  // 4 KiB staging tiles per epilogue warp
+  static constexpr int kStages = MODE == GATED_SLOPES ? 5 : 6;
+  static constexpr int kEpiBytes = GP_EPI_WARPS * kStaging * 4096;
+  static constexpr int kSmem = kStages * STAGE_BYTES + kEpiBytes + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+template <int ACT>
+__device__ __forceinline__ void gate_row(const uint32_t (&g)[32], const uint32_t (&u)[32], bool fp16,
+                                         uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float lo = act_value<ACT>(__uint_as_float(g[2 * q])) * __uint_as_float(u[2 * q]);
+    const float hi = act_value<ACT>(__uint_as_float(g[2 * q + 1])) * __uint_as_float(u[2 * q + 1]);
+    pk[q] = fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+  }
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<__half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// dg and du for a row's 32 columns; d: the row's dH.
+template <int ACT>
+__device__ __forceinline__ void slope_row(const uint32_t (&g)[32], const uint32_t (&u)[32], const uint32_t (&d)[16],
+                                          bool fp16, uint32_t (&dg)[16], uint32_t (&du)[16]) {
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float2 h = unpack16(d[q], fp16);
+    const ActSlope lo = act_slope<ACT>(__uint_as_float(g[2 * q])), hi = act_slope<ACT>(__uint_as_float(g[2 * q + 1]));
+    const float g0 = h.x * __uint_as_float(u[2 * q]) * lo.slope;
+    const float g1 = h.y * __uint_as_float(u[2 * q + 1]) * hi.slope;
+    const float u0 = h.x * lo.value, u1 = h.y * hi.value;
+    dg[q] = fp16 ? pack_f16x2(g0, g1) : pack_bf16x2(g0, g1);
+    du[q] = fp16 ? pack_f16x2(u0, u1) : pack_bf16x2(u0, u1);
+  }
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(saddr) : "memory");
+}
+
+// A row's 32 columns (64 bytes: 16-byte chunks 4h .. 4h + 3) of a 32 x 64
+// staging tile in the 128-byte swizzle.
+__device__ __forceinline__ void stage_row(uint32_t row_addr, int lane, int h, const uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(row_addr + (uint32_t)((((h * 4 + q) ^ (lane & 7)) * 16)), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2],
+                 pk[4 * q + 3]);
+}
+
+// The columns of a row's 32 (from column n) that lie in [tail, cols).
+__device__ __forceinline__ void store_tail(const GatedPairParams& p, int out, int row, int n,
+                                           const uint32_t (&pk)[16]) {
+  if (p.tail >= n + 32 || p.cols <= n || p.tail >= p.cols || row >= p.rows) return;
+  uint16_t* at = p.out[out] + (int64_t)row * p.ld[out] + n;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    if (n + 2 * q >= p.tail && n + 2 * q < p.cols) at[2 * q] = (uint16_t)pk[q];
+    if (n + 2 * q + 1 >= p.tail && n + 2 * q + 1 < p.cols) at[2 * q + 1] = (uint16_t)(pk[q] >> 16);
+  }
+}
+
+}  // namespace
+
+// Tile t of the launch: which output (WEIGHTS) and part of the reduction,
+// and where.
+struct TileAt {
+  int out, part, mb, nb, k0, k1;
+};
+template <int MODE>
+__device__ __forceinline__ TileAt tile_at(int t, const GatedPairParams& p) {
+  TileAt a;
+  const int per = p.tiles_m * p.tiles_n;
+  const int outer = t / per;
+  a.out = outer / p.parts;
+  a.part = outer - a.out * p.parts;
+  tile_coords(t - outer * per, p.tiles_m, p.tiles_n, p.raster_g, a.mb, a.nb);
+  a.k0 = (int)((int64_t)p.ksteps * a.part / p.parts);
+  a.k1 = (int)((int64_t)p.ksteps * (a.part + 1) / p.parts);
+  return a;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(GP_THREADS, 1)
+    gated_pair_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedPairParams p) {
+  using C = Cfg<MODE>;
+  constexpr int STAGES = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_a = base;
+  uint8_t* s_b = s_a + STAGES * OPERAND_BYTES;
+  uint8_t* s_epi = s_b + STAGES * OPERAND_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + C::kEpiBytes);  // even CTA: both CTAs' copies
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;
+  uint64_t* acce = accf + 2;  // even CTA only: both CTAs have read the accumulator
+  uint64_t* drain = acce + 2;
+  uint64_t* dh_bar = drain + 1;  // SLOPES: one per epilogue warp, its dH tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dh_bar + GP_EPI_WARPS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = (int)(blockIdx.x >> 1);
+  const int npairs = (int)(gridDim.x >> 1);
+  const uint64_t limit = p.wait_limit_ns;
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+
+  // This CTA's 128 rows of A, and of B, for reduction step ks.
+  auto load_a = [&](int st, const TileAt& a, int ks) {
+    const uint32_t bar = full_leader + (uint32_t)(st * 8);
+    uint8_t* dst = s_a + st * OPERAND_BYTES;
+    const int row = a.mb * 256 + rank * 128;
+    if constexpr (MODE == GATED_WEIGHTS) {
+      tma_load_2d_pair(dst, &maps.a[a.out], row, ks * 64, bar);
+      tma_load_2d_pair(dst + MN_BLOCK_BYTES, &maps.a[a.out], row + 64, ks * 64, bar);
+    } else if constexpr (MODE == GATED_INPUT) {
+      const int half = ks >= p.ksteps_half ? 1 : 0;
+      tma_load_2d_pair(dst, &maps.a[half], (ks - half * p.ksteps_half) * 64, row, bar);
+    } else {
+      tma_load_2d_pair(dst, &maps.a[0], ks * 64, row, bar);
+    }
+  };
+  auto load_b = [&](int st, const TileAt& a, int ks) {
+    const uint32_t bar = full_leader + (uint32_t)(st * 8);
+    uint8_t* dst = s_b + st * OPERAND_BYTES;
+    if constexpr (C::kGate) {
+      tma_load_2d_pair(dst, &maps.b[rank], ks * 64, a.nb * 128, bar);
+    } else {
+      const int half = MODE == GATED_INPUT && ks >= p.ksteps_half ? 1 : 0;
+      const int col = a.nb * 256 + rank * 128, k = (ks - half * p.ksteps_half) * 64;
+      tma_load_2d_pair(dst, &maps.b[half], col, k, bar);
+      tma_load_2d_pair(dst + MN_BLOCK_BYTES, &maps.b[half], col + 64, k, bar);
+    }
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 2);  // the even CTA's A and B issuers (unused in the odd CTA)
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 2 * GP_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    for (int w = 0; w < GP_EPI_WARPS; ++w) mbar_init(&dh_bar[w], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair<512>(tmem_slot);
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated before any remote access
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t peer_base = ld_shared_cluster_u32(mapa_shared(smem_u32(tmem_slot), (uint32_t)rank ^ 1u));
+  const bool bad = tmem_base != peer_base;
+  if (bad && leader && threadIdx.x == 0) atomicOr(p.status, ST_BAD_LAUNCH);
+
+  // With constant weights the B issuer requests B for the first stages of its
+  // first tile before the wait on the previous kernel; A follows after.
+  int early = 0;
+  if (MODE == GATED_FORWARD && !bad && p.b_constant && pair < p.num_tiles && threadIdx.x == 0) {
+    const TileAt a = tile_at<MODE>(pair, p);
+    early = min(a.k1 - a.k0, STAGES);
+    for (int i = 0; i < early; ++i) {
+      if (p.debug_skip_load == 1 + i) continue;
+      if (leader) mbar_arrive_expect_tx(&full[i], 2 * OPERAND_BYTES);
+      load_b(i, a, a.k0 + i);
+    }
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (bad) {
+    // nothing to do: fall through to the final cluster barrier
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producers
+    if (lane < 2) {
+      const bool is_b = lane == 0;
+      int s = 0;
+      uint32_t ph = 0, issued = 0;
+      bool ok = true;
+      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
+        const TileAt a = tile_at<MODE>(t, p);
+        for (int ks = a.k0; ks < a.k1; ++ks) {
+          const bool done = is_b && (int)issued < early;
+          if (!done && !wait_bounded(&empty[s], ph ^ 1, abort_flag, p.status, ST_TIMEOUT_PRODUCER, limit)) {
+            ok = false;
+            break;
+          }
+          if (p.debug_skip_load == 1 + (int)issued) {
+            // Fault injection (host-selected): leave this stage's barrier
+            // without its arrivals, so the waits on it time out.
+          } else if (!done) {
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * OPERAND_BYTES);
+            if (is_b)
+              load_b(s, a, ks);
+            else
+              load_a(s, a, ks);
+          }
+          ++issued;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (leader && (!ok || *abort_flag)) {
+        // Wait (bounded) for the loads still in flight, so nothing lands in
+        // shared memory after exit.
+        const uint32_t n = issued < (uint32_t)STAGES ? issued : (uint32_t)STAGES;
+        for (uint32_t i = 0; i < n; ++i) {
+          const uint32_t q = issued - 1 - i;
+          volatile int never = 0;
+          if (p.debug_skip_load == 1 + (int)q) continue;
+          wait_bounded(&full[q % STAGES], (q / STAGES) & 1, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t idesc = idesc_dense(p.fp16 ? 0u : 1u, p.fp16 ? 0u : 1u, 256, 256) | (C::kAMn ? kIdescAMn : 0u) |
+                             (C::kBMn ? kIdescBMn : 0u);
+      int s = 0;
+      uint32_t ph = 0;
+      int local = 0;
+      bool ok = true;
+      for (int t = pair; t < p.num_tiles && ok; t += npairs, ++local) {
+        const TileAt a = tile_at<MODE>(t, p);
+        const int buf = local & 1;
+        if (!wait_cluster_bounded(&acce[buf], ((uint32_t)(local >> 1) & 1) ^ 1, abort_flag, p.status, ST_TIMEOUT_MMA,
+                                  limit))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+        for (int ks = a.k0; ks < a.k1; ++ks) {
+          if (!wait_cluster_bounded(&full[s], ph, abort_flag, p.status, ST_TIMEOUT_MMA, limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(s_a + s * OPERAND_BYTES);
+          const uint32_t b0 = smem_u32(s_b + s * OPERAND_BYTES);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = C::kAMn ? smem_desc_sw128_mn(a0 + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(a0 + 32 * k);
+            const uint64_t bd = C::kBMn ? smem_desc_sw128_mn(b0 + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(b0 + 32 * k);
+            umma_pair<0>(d, ad, bd, idesc, (ks > a.k0 || k > 0) ? 1u : 0u);
+          }
+          umma_commit_pair(&empty[s], 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(&accf[buf], 0x3);
+      }
+      // Every issued MMA must complete before either CTA releases TMEM.
+      umma_commit_pair(drain, 0x1);
+      volatile int never = 0;
+      wait_bounded(drain, 0, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;         // TMEM lanes this warp may access: quad*32 .. +31
+    const int chalf = (warp - 2) / 4;  // this warp takes the 64-column chunks c with c % 2 == chalf
+    uint8_t* stg = s_epi + (warp - 2) * (C::kStaging * 4096);
+    uint8_t* stg2 = stg + 4096;  // SLOPES
+    const uint32_t stg_row = smem_u32(stg) + lane * 128;
+    const uint32_t acce_leader = mapa_shared(smem_u32(acce), 0);
+    const bool fp16 = p.fp16 != 0;
+    uint64_t* dhb = &dh_bar[warp - 2];
+    uint32_t dh_phase = 0;
+    int local = 0;
+    for (int t = pair; t < p.num_tiles; t += npairs, ++local) {
+      const TileAt a = tile_at<MODE>(t, p);
+      const int buf = local & 1;
+      const int row0 = a.mb * 256 + rank * 128 + quad * 32;
+      const uint32_t tbase = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * 256);
+      [[maybe_unused]] bool dh_wanted = false;
+      if constexpr (MODE == GATED_SLOPES) {
+        // This warp's dH tile, requested while the tile's MMAs still run,
+        // into the staging tile that dg will leave from.
+        const int n0 = a.nb * 128 + chalf * 64;
+        dh_wanted = row0 < p.rows && n0 < p.cols;
+        if (lane == 0) bulk_wait_group_read<0>();  // the previous stores have read the staging tiles
+        if (dh_wanted && lane == 0) {
+          mbar_arrive_expect_tx(dhb, 4096);
+          tma_load_2d(stg, &maps.dh, n0, row0, dhb);
+        }
+        __syncwarp();
+      }
+      if (!wait_bounded(&accf[buf], (uint32_t)(local >> 1) & 1, abort_flag, p.status, ST_TIMEOUT_EPILOGUE, limit)) {
+        if (dh_wanted) {  // let the copy land before the kernel ends
+          volatile int never = 0;
+          wait_bounded(dhb, dh_phase, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+        }
+        break;
+      }
+      tc_fence_after();
+      if constexpr (C::kGate) {
+        const int n0 = a.nb * 128 + chalf * 64;
+        const bool inside = row0 < p.rows && n0 < (MODE == GATED_SLOPES ? p.cols : p.tail);
+        if constexpr (MODE == GATED_SLOPES) {
+          if (dh_wanted) {
+            if (!wait_bounded(dhb, dh_phase, abort_flag, p.status, ST_TIMEOUT_EPILOGUE, limit)) break;
+            dh_phase ^= 1;
+          }
+        } else {
+          if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the staging tile
+          __syncwarp();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t g[32], u[32];
+          tmem_ld_32x32b_x32(tbase + (uint32_t)(chalf * 64 + h * 32), g);
+          tmem_ld_32x32b_x32(tbase + (uint32_t)(128 + chalf * 64 + h * 32), u);
+          tmem_ld_wait();
+          if (h == 1) {  // this warp's last loads of the accumulator: free it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acce_leader + (uint32_t)(buf * 8));
+          }
+          if constexpr (MODE == GATED_SLOPES) {
+            uint32_t d[16], dg[16], du[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              ld_shared_v4(stg_row + (uint32_t)((((h * 4 + q) ^ (lane & 7)) * 16)), d[4 * q], d[4 * q + 1],
+                           d[4 * q + 2], d[4 * q + 3]);
+            switch (p.act) {
+              case GP_ACT_RELU: slope_row<GP_ACT_RELU>(g, u, d, fp16, dg, du); break;
+              case GP_ACT_SILU: slope_row<GP_ACT_SILU>(g, u, d, fp16, dg, du); break;
+              default: slope_row<GP_ACT_GELU>(g, u, d, fp16, dg, du); break;
+            }
+            stage_row(stg_row, lane, h, dg);  // each lane overwrites what it alone read
+            stage_row(stg_row + 4096, lane, h, du);
+          } else {
+            uint32_t pk[16];
+            switch (p.act) {
+              case GP_ACT_RELU: gate_row<GP_ACT_RELU>(g, u, fp16, pk); break;
+              case GP_ACT_SILU: gate_row<GP_ACT_SILU>(g, u, fp16, pk); break;
+              default: gate_row<GP_ACT_GELU>(g, u, fp16, pk); break;
+            }
+            stage_row(stg_row, lane, h, pk);
+            store_tail(p, 0, row0 + lane, n0 + h * 32, pk);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && inside) {
+          tma_store_2d(&maps.c[0], n0, row0, stg);
+          if (MODE == GATED_SLOPES) tma_store_2d(&maps.c[1], n0, row0, stg2);
+          bulk_commit_group();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = chalf; c < 4; c += 2) {
+          const int n0 = a.nb * 256 + c * 64;
+          const bool inside = row0 < p.rows && n0 < p.tail;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tbase + (uint32_t)(c * 64 + h * 32), r);
+            tmem_ld_wait();
+            if (c + 2 >= 4 && h == 1) {  // this warp's last loads of the accumulator: free it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote(acce_leader + (uint32_t)(buf * 8));
+            }
+            if (p.parts > 1) {
+              // fp32 sums of this part: a 32 x 32 tile, 128 bytes a row
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                st_shared_v4(stg_row + (uint32_t)(((q ^ (lane & 7)) * 16)), r[4 * q], r[4 * q + 1], r[4 * q + 2],
+                             r[4 * q + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && row0 < p.rows && n0 + h * 32 < p.cols) {
+                tma_store_3d(&maps.partial, n0 + h * 32, row0, a.out * p.parts + a.part, stg);
+                bulk_commit_group();
+              }
+            } else {
+              if (h == 0) {
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+              }
+              uint32_t pk[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                const float lo = __uint_as_float(r[2 * q]), hi = __uint_as_float(r[2 * q + 1]);
+                pk[q] = fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+              }
+              stage_row(stg_row, lane, h, pk);
+              store_tail(p, a.out, row0 + lane, n0 + h * 32, pk);
+            }
+          }
+          if (p.parts == 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && inside) {
+              tma_store_2d(&maps.c[a.out], n0, row0, stg);
+              bulk_commit_group();
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group_read<0>();  // staging read; the writes complete with the grid
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // no CTA touches its peer's shared or tensor memory after this
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair<512>(tmem_base);
+  }
+}
+
+namespace {
+
+// out[r, c] = sum of the parts' fp32 sums, in order, rounded once.  blockIdx.y
+// is the output (WEIGHTS has two).
+__global__ void __launch_bounds__(256) gated_add_parts_kernel(const float4* partial, int parts, int64_t rows,
+                                                              int64_t quads, int64_t cols, uint16_t* out0, int64_t ld0,
+                                                              uint16_t* out1, int64_t ld1, int fp16) {
+  pdl_launch_dependents();
+  pdl_wait();
+  uint16_t* out = blockIdx.y == 0 ? out0 : out1;
+  const int64_t ld = blockIdx.y == 0 ? ld0 : ld1;
+  const int64_t slice = rows * quads;
+  partial += blockIdx.y * parts * slice;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < slice; x += step) {
+    float4 v = partial[x];
+    for (int s = 1; s < parts; ++s) {
+      const float4 w = partial[s * slice + x];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    const int64_t r = x / quads, c = (x - r * quads) * 4;
+    const uint32_t lo = fp16 ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
+    const uint32_t hi = fp16 ? pack_f16x2(v.z, v.w) : pack_bf16x2(v.z, v.w);
+    uint16_t* at = out + r * ld + c;
+    if (c + 4 <= cols) {  // rows start on 16-byte boundaries, c on a multiple of 4
+      *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi);
+    } else {
+      const uint32_t w[2] = {lo, hi};
+      for (int e = 0; e < cols - c; ++e) at[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
+template <int MODE>
+int launch_mode(const GatedMaps& maps, GatedPairParams p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<MODE>;
+  auto kern = gated_pair_kernel<MODE>;
+  static std::atomic<bool> attr_set[64];
+  if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
+  const int pairs = num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (p.num_tiles < pairs ? p.num_tiles : pairs)));
+  cfg.blockDim = dim3(GP_THREADS);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, p) != cudaSuccess) return GP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
+}
+
+}  // namespace
+
+int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p, int num_sms, cudaStream_t stream) {
+  switch (mode) {
+    case GATED_FORWARD: return launch_mode<GATED_FORWARD>(maps, p, num_sms, stream);
+    case GATED_SLOPES: return launch_mode<GATED_SLOPES>(maps, p, num_sms, stream);
+    case GATED_INPUT: return launch_mode<GATED_INPUT>(maps, p, num_sms, stream);
+    default: return launch_mode<GATED_WEIGHTS>(maps, p, num_sms, stream);
+  }
+}
+
+int gated_add_parts_launch(const float* partial, int parts, int outputs, int64_t rows, int64_t cols, int64_t pitch,
+                           void* out0, int64_t ld0, void* out1, int64_t ld1, bool fp16, int num_sms,
+                           cudaStream_t stream) {
+  const int64_t quads = pitch / 4;
+  int64_t blocks = (rows * quads + 255) / 256;
+  const int64_t most = (int64_t)num_sms * 8;
+  if (blocks > most) blocks = most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)outputs);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, gated_add_parts_kernel, reinterpret_cast<const float4*>(partial), parts, rows, quads,
+                         cols, static_cast<uint16_t*>(out0), ld0, static_cast<uint16_t*>(out1), ld1,
+                         fp16 ? 1 : 0) != cudaSuccess)
+    return GP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
+}
+
+}  // namespace gp

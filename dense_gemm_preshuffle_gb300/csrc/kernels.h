@@ -41,6 +41,10 @@ int host_context(HostContext* out);
 // `row_bytes` apart, boxes of box_inner x box_outer elements.
 int encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+// Its 3-D form: `slices` such matrices, slice_bytes apart.
+int encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint64_t inner, uint64_t outer,
+                  uint64_t slices, uint64_t row_bytes, uint64_t slice_bytes, uint32_t box_inner, uint32_t box_outer,
+                  uint32_t box_slices, CUtensorMapSwizzle swz);
 // The armed index of gemm_debug_skip_load, which this call disarms.
 int take_debug_skip_load();
 

@@ -210,6 +210,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t x, 
                : "memory");
 }
 
+// 3-D tiled TMA store (x, y, z) from shared memory.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                             const void* smem_src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+               : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until at most N committed bulk groups still read shared memory.
@@ -289,6 +298,25 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   d |= (uint64_t)2 << 61;                         // swizzle mode: 128-byte
   return d;
 }
+
+// Shared-memory matrix descriptor for an MN-major 16-bit operand stored in
+// the 128-byte-swizzled canonical layout: blocks of 64 (M or N) values, one
+// 128-byte line for each k, eight lines to a 1024-byte group (stride byte
+// offset); the next 64 values are `block_bytes` further on (leading byte
+// offset).  Advancing K by 16 adds 2048 bytes to the address.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(block_bytes >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Instruction descriptor bits for MN-major A and B (16-bit kinds).
+constexpr uint32_t kIdescAMn = 1u << 15;
+constexpr uint32_t kIdescBMn = 1u << 16;
 
 // Instruction descriptor for kind::f16 / kind::f8f6f4 (dense, K-major A and B,
 // fp32 accumulator).
