@@ -303,34 +303,49 @@ def matmul(A, B_packed, dtype, N: int, K: int, scale_a=None, scale_b=None, out=N
     return out
 
 
+_float16_types = None
+
+
 def _float16_type(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DTYPES["bf16"]
-    if t.dtype == torch.float16:
-        return DTYPES["fp16"]
-    raise ValueError(f"a bf16 or fp16 tensor is wanted: got {t.dtype}")
+    global _float16_types
+    if _float16_types is None:
+        import torch
+        _float16_types = {torch.bfloat16: DTYPES["bf16"], torch.float16: DTYPES["fp16"]}
+    code = _float16_types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"a bf16 or fp16 tensor is wanted: got {t.dtype}")
+    return code
 
 
 def _matrix(name: str, t, shape, dtype) -> int:
     """Checks a device matrix with contiguous rows and returns its row pitch."""
-    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: a {dtype} CUDA tensor of shape {shape} is wanted, got {t.dtype} "
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name}: a {dtype} CUDA tensor of shape {tuple(shape)} is wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
+    rows, cols = shape
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: its rows are not contiguous (strides {t.stride()})")
-    if shape[0] <= 1 or shape[1] == 0:  # a single row's pitch is never used, nor are empty rows
-        return (max(ld, shape[1]) + 7) // 8 * 8
+    if rows <= 1 or cols == 0:  # a single row's pitch is never used, nor are empty rows
+        return (max(ld, cols) + 7) // 8 * 8
     return ld
 
 
 def _new_rows(like, rows: int, cols: int):
     """An empty [rows, cols] matrix of like's type whose rows start on 16-byte boundaries."""
-    import torch
-    ld = (cols + 7) // 8 * 8
-    t = torch.empty((rows, ld), dtype=like.dtype, device=like.device)
-    return t if ld == cols else t[:, :cols]
+    if cols % 8 == 0:
+        return like.new_empty((rows, cols))
+    return like.new_empty((rows, (cols + 7) // 8 * 8))[:, :cols]
+
+
+def _stream_for(t, stream) -> Optional[int]:
+    """The launch stream: `stream`, or torch's current one on t's device.
+    (The raw handle: building torch's Stream object takes 3 us of host time,
+    as long as a small product.)"""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_constant: bool = False):
@@ -341,15 +356,16 @@ def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_co
     slice of a wider buffer will do).  act is "silu", "gelu" or "relu".
     Returns H [M, N]; where N % 8 != 0 a new H is a slice of a wider buffer.
     b_constant=True: no GPU work still in flight writes the weights."""
-    dt = _float16_type(A)
+    dt, t = _float16_type(A), A.dtype
     M, K = A.shape
     N = W_gate.shape[0]
-    t = A.dtype
+    lda, ldg, ldu = _matrix("A", A, (M, K), t), _matrix("W_gate", W_gate, (N, K), t), _matrix("W_up", W_up, (N, K), t)
     if out is None:
         out = _new_rows(A, M, N)
-    gemm_gated_run(A, _matrix("A", A, (M, K), t), W_gate, _matrix("W_gate", W_gate, (N, K), t), W_up,
-                   _matrix("W_up", W_up, (N, K), t), dt, M, N, K, act, out, _matrix("out", out, (M, N), t),
-                   GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, stream)
+    _check((_lib or load_library()).gemm_gated_run(
+        A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dt, M, N, K, _act(act), out.data_ptr(),
+        _matrix("out", out, (M, N), t), GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT,
+        _stream_for(A, stream)), "gemm_gated_run")
     return out
 
 
@@ -360,33 +376,36 @@ def gated_matmul_backward(A, W_gate, W_up, dH, act: str = "silu", need_dA: bool 
     Returns (dA, dW_gate, dW_up) of A's type, with None for what is not
     needed.  The inputs' products are computed again, so nothing but the
     inputs is kept between the two passes.  out: the three tensors (or None)
-    to write into.  workspace: a uint8 device tensor of at least
+    to write into.  workspace: a contiguous device tensor of at least
     gemm_gated_backward_workspace_bytes(M, N, K) bytes; by default one is
     allocated for the call."""
-    import torch
-    dt = _float16_type(A)
+    dt, t = _float16_type(A), A.dtype
     M, K = A.shape
     N = W_gate.shape[0]
-    t = A.dtype
+    lda, ldg, ldu = _matrix("A", A, (M, K), t), _matrix("W_gate", W_gate, (N, K), t), _matrix("W_up", W_up, (N, K), t)
+    lddh = _matrix("dH", dH, (M, N), t)
     dA, dG, dU = out if out is not None else (None, None, None)
-    if need_dA and dA is None:
-        dA = _new_rows(A, M, K)
-    if need_dW and dG is None:
-        dG = _new_rows(A, N, K)
-    if need_dW and dU is None:
-        dU = _new_rows(A, N, K)
     if not need_dA:
         dA = None
+    elif dA is None:
+        dA = _new_rows(A, M, K)
     if not need_dW:
         dG = dU = None
+    else:
+        dG = _new_rows(A, N, K) if dG is None else dG
+        dU = _new_rows(A, N, K) if dU is None else dU
     if workspace is None:
-        workspace = torch.empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=A.device)
-    gemm_gated_backward(A, _matrix("A", A, (M, K), t), W_gate, _matrix("W_gate", W_gate, (N, K), t), W_up,
-                        _matrix("W_up", W_up, (N, K), t), dH, _matrix("dH", dH, (M, N), t), dt, M, N, K, act,
-                        dA, 0 if dA is None else _matrix("dA", dA, (M, K), t),
-                        dG, 0 if dG is None else _matrix("dW_gate", dG, (N, K), t),
-                        dU, 0 if dU is None else _matrix("dW_up", dU, (N, K), t),
-                        workspace, workspace.numel() * workspace.element_size(), stream)
+        import torch
+        workspace = A.new_empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous CUDA tensor is wanted")
+    _check((_lib or load_library()).gemm_gated_backward(
+        A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dH.data_ptr(), lddh, dt, M, N, K, _act(act),
+        _ptr(dA), 0 if dA is None else _matrix("dA", dA, (M, K), t),
+        _ptr(dG), 0 if dG is None else _matrix("dW_gate", dG, (N, K), t),
+        _ptr(dU), 0 if dU is None else _matrix("dW_up", dU, (N, K), t),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_for(A, stream)),
+        "gemm_gated_backward")
     return dA, dG, dU
 
 
@@ -435,15 +454,17 @@ def unpack_w4g(W: W4Weights, stream=None):
     return codes, scales, zeros
 
 
-def _run_w4g(A, W: W4Weights, U: Optional[W4Weights], act, out, stream, b_constant: bool):
-    import torch
-    dt = _float16_type(A)
+def _run_w4g(A, W: W4Weights, U: Optional[W4Weights], act: int, out, stream, b_constant: bool):
+    dt, t = _float16_type(A), A.dtype
+    packed, N, K, group, scale_dtype, has_zeros = W
     M = A.shape[0]
+    lda = _matrix("A", A, (M, K), t)
     if out is None:
-        out = torch.empty((M, W.N), dtype=A.dtype, device=A.device)
-    lda, ldc = _matrix("A", A, (M, W.K), A.dtype), _matrix("out", out, (M, W.N), A.dtype)
-    gemm_run_w4g(A, lda, dt, W.packed, None if U is None else U.packed, W.scale_dtype, W.has_zeros, M, W.N, W.K,
-                 W.group, act, out, ldc, GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, stream)
+        out = A.new_empty((M, N))
+    _check((_lib or load_library()).gemm_run_w4g(
+        A.data_ptr(), lda, dt, packed.data_ptr(), None if U is None else U.packed.data_ptr(), scale_dtype, has_zeros,
+        M, N, K, group, act, out.data_ptr(), _matrix("out", out, (M, N), t),
+        GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, _stream_for(A, stream)), "gemm_run_w4g")
     return out
 
 
@@ -451,13 +472,13 @@ def matmul_w4g(A, W: W4Weights, out=None, stream=None, b_constant: bool = False)
     """C = A . W^T for a few rows of A [M, K] (bf16 or fp16) and packed 4-bit
     weights; returns [M, N] of A's type.  b_constant=True: no GPU work still
     in flight writes the packed weights (pack once, then synchronise)."""
-    return _run_w4g(A, W, None, None, out, stream, b_constant)
+    return _run_w4g(A, W, None, 0, out, stream, b_constant)
 
 
 def matmul_w4g_gated(A, W_gate: W4Weights, W_up: W4Weights, act: str = "silu", out=None, stream=None,
                      b_constant: bool = False):
     """act(A . W_gate^T) * (A . W_up^T) with both weights packed in 4 bits
     (of one shape, group, scale type and kind of zero points)."""
-    if tuple(W_gate[1:]) != tuple(W_up[1:]):
-        raise ValueError(f"W_gate and W_up differ: {tuple(W_gate[1:])} and {tuple(W_up[1:])}")
-    return _run_w4g(A, W_gate, W_up, act, out, stream, b_constant)
+    if W_gate[1:] != W_up[1:]:
+        raise ValueError(f"W_gate and W_up differ: {W_gate[1:]} and {W_up[1:]}")
+    return _run_w4g(A, W_gate, W_up, _act(act), out, stream, b_constant)

@@ -145,6 +145,7 @@ int map_parts(CUtensorMap* map, float* partial, int64_t slices, int64_t rows, in
 size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K) { return (size_t)workspace_of(M, N, K).bytes; }
 
 int gated_run_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
+  if (a.M <= kGatedStreamRows) return gated_stream_launch(a, ctx, stream);
   return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, stream);
 }
 

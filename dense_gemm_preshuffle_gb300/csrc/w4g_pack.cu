@@ -30,7 +30,7 @@ __device__ __forceinline__ int64_t word_offset(int64_t n, int64_t c, int i, int 
 __device__ __forceinline__ int64_t scale_offset(int64_t n, int64_t j, int gpb, int64_t kblocks) {
   const int64_t block = (n >> 4) * kblocks + j / gpb;
   const int h = (int)(n >> 3) & 1, g = (int)n & 7;
-  return (block * gpb + j % gpb) * 16 + 2 * g + h;
+  return ((block * 8 + g) * gpb + j % gpb) * 2 + h;
 }
 
 // Eight codes k0..k7 in the low-nibble-first order of a row -> the packed

@@ -377,8 +377,8 @@ int gemm_packed_w4g_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t
  *   - codes, 1024 bytes a block: the 32-bit word i (0..3) of lane 4g + t and
  *     half h, at byte (h*32 + 4g + t)*16 + 4i, holds row 16r + 8h + g,
  *     k0 = 128c + 32i + 8t: codes k0..k0+7 at bits 0, 16, 4, 20, 8, 24, 12, 28.
- *   - scales: 16 * 128/group values a block, group by group; within a group
- *     row 8h + g is at 2g + h.
+ *   - scales: 16 * 128/group values a block; the one of row 8h + g, group j
+ *     of the block, is at (g * 128/group + j)*2 + h.
  *   - zero points, where given: bytes in the scales' order.
  * One kernel on `stream`.
  */

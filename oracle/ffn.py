@@ -186,7 +186,7 @@ def w4g_pack(codes: np.ndarray, scales_bits: np.ndarray, zeros: Optional[np.ndar
                 w |= int(q[n, k0 + e]) << place[e]
             words[(r * kb + c) * 256 + (h * 32 + 4 * g + t) * 4 + i] = w
         for j in range(scales_bits.shape[1]):
-            at = ((r * kb + j // gpb) * gpb + j % gpb) * 16 + 2 * g + h
+            at = (((r * kb + j // gpb) * 8 + g) * gpb + j % gpb) * 2 + h
             sc[at] = scales_bits[n, j]
             if zeros is not None:
                 zp[at] = zeros[n, j]
