@@ -7,12 +7,16 @@ namespace gp {
 
 namespace {
 
+template <bool FP16, int NT>
+int launch_nt(const StreamParams& p, int num_sms, cudaStream_t stream) {
+  return launch_stream<Rows16<FP16, 2, 1, 8>, 2, 1, NT, 3, 8, 2>(p, num_sms, stream);
+}
+
 template <bool FP16>
 int launch_type(const StreamParams& p, int num_sms, cudaStream_t stream) {
-  using P = Rows16<FP16>;
-  if (p.M <= 8) return launch_stream<P, 2, 1, 1, 3, 8, 2>(p, num_sms, stream);
-  if (p.M <= 16) return launch_stream<P, 2, 1, 2, 3, 8, 2>(p, num_sms, stream);
-  return launch_stream<P, 2, 1, 4, 3, 8, 2>(p, num_sms, stream);
+  if (p.M <= 8) return launch_nt<FP16, 1>(p, num_sms, stream);
+  if (p.M <= 16) return launch_nt<FP16, 2>(p, num_sms, stream);
+  return launch_nt<FP16, 4>(p, num_sms, stream);
 }
 
 }  // namespace
@@ -30,7 +34,8 @@ int gated_stream_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t
   p.M = (int)a.M;
   p.N = (int)a.N;
   p.K = (int)a.K;
-  p.steps = (int)((a.K + Rows16<false>::kStepK - 1) / Rows16<false>::kStepK);
+  constexpr int kStepK = Rows16<false, 2, 1, 8>::kStepK;
+  p.steps = (int)((a.K + kStepK - 1) / kStepK);
   p.row_tiles = (int)((a.N + 15) / 16);
   p.act = a.act;
   p.b_constant = a.b_constant ? 1 : 0;

@@ -176,11 +176,10 @@ struct W4gArgs {
   int64_t ldc;
   bool b_constant;
 };
-// Byte offsets of the scale and zero-point regions of a packed buffer, and
-// its size.
+// The packed buffer: blocks of 16 rows x 128 values.
 struct W4gLayout {
-  int64_t row_tiles, kblocks;  // ceil(N / 16), ceil(K / 128)
-  int64_t scales, zeros, bytes;
+  int64_t row_tiles, kblocks;  // tiles of 16 rows, N rounded up to 64; ceil(K / 128)
+  int64_t block_bytes, bytes;
 };
 W4gLayout w4g_layout(int64_t N, int64_t K, int group, bool has_zeros);
 int w4g_pack_launch(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t K,

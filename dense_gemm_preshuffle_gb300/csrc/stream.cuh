@@ -7,9 +7,9 @@
 //   - A step is one warp's work on R tiles of 16 weight rows (of W, and with
 //     MATS = 2 of U): every lane fetches, with 16-byte cp.async, exactly the
 //     bytes that its own mma.sync fragments need, into a ring of its own in
-//     shared memory, and reads only those back.  There are no barriers and
-//     no producer: cp.async.wait_group orders a lane with itself, and STAGES
-//     steps of every warp are in flight.
+//     shared memory, and reads only those back (but for the scales of 4-bit
+//     weights, which a warp shares).  There is no producer and no barrier
+//     among warps, and STAGES - 1 steps of every warp are in flight.
 //   - The weights are the MMA's 16-row operand and A's rows its 8 columns
 //     (NT such groups), so that M = 1..8 costs one MMA.  K is permuted alike
 //     for both: lane t of a row's four takes 8 consecutive values, which are
@@ -38,7 +38,8 @@ struct StreamParams {
   int64_t ldw[2];            // 16-bit rows: elements
   uint16_t* C;
   int64_t ldc;
-  int64_t scales, zeros;     // 4 bits: byte offsets of these regions; zeros 0: 8 throughout
+  int block_bytes;           // 4 bits: codes, scales and zero points of 16 rows x 128 values
+  int has_zeros;             // 4 bits: else 8 throughout
   int M, N, K;
   int steps;                 // steps of a row tile
   int row_tiles;             // ceil(N / 16)
@@ -67,6 +68,22 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "one vector load");
+  if constexpr (N == 1)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
 // d += a (16 rows x 16) . b (16 x 8), fp32 sums.
 template <bool FP16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -81,21 +98,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight values of row m of A from k on, as four pairs; zeros past M or K.
-template <bool CHECK_K>
-__device__ __forceinline__ uint4 load_a8(const uint16_t* row, bool in, int k, int K) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (!in) return v;
-  if (!CHECK_K || k + 8 <= K) {
-    v = __ldg(reinterpret_cast<const uint4*>(row + k));
-  } else if (k < K) {  // a row's last, short run of values
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+// Eight values of a row of A from k on, as four pairs; zeros from K on.
+__device__ __forceinline__ uint4 load_a8(const uint16_t* row, int k, int K) {
+  if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k + e < K) w[e / 2] |= (uint32_t)__ldg(row + k + e) << (16 * (e & 1));
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return v;
+  for (int e = 0; e < 8; ++e)
+    if (k + e < K) w[e / 2] |= (uint32_t)__ldg(row + k + e) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float act_of(float v, int act) {
@@ -110,120 +120,137 @@ __device__ __forceinline__ float act_of(float v, int act) {
 // A policy fetches a lane's bytes of a step and multiplies them:
 //   kStepK     K values of a step
 //   kBytes     ring bytes of a step and row tile
-//   Extra      what a step needs besides the ring, loaded one step ahead
-//   fetch / extra / multiply
+//   Cursor     where the lane's next bytes are (WARPS steps on from the last)
+//   kShared    whether a lane reads bytes that another one fetched
+// Row tiles past the last are never addressed: 16-bit rows past N are read
+// as row N - 1, packed weights are padded, and neither's sums are stored.
 
-// 16-bit rows as the caller has them: row g and row g + 8 of a tile, 16
-// bytes a lane and half step of 32 values.
-template <bool FP16_>
+// 16-bit rows as the caller has them: rows g and g + 8 of a tile, 16 bytes a
+// lane and 32 values.
+template <bool FP16_, int MATS, int R, int WARPS>
 struct Rows16 {
+  static_assert(R == 1, "one row tile of each matrix");
   static constexpr bool FP16 = FP16_;
-  static constexpr int kHalves = 2;
+  static constexpr int kHalves = 2;  // 128 contiguous bytes of a row
   static constexpr int kStepK = 32 * kHalves;
   static constexpr int kBytes = 1024 * kHalves;
-  static constexpr bool kCheckK = true;
-  struct Extra {};
+  static constexpr bool kShared = false;
 
-  static __device__ __forceinline__ void fetch(const StreamParams& p, int mat, int tile, int step, uint32_t dst,
-                                               int lane) {
-    const int64_t n = (int64_t)tile * 16 + (lane >> 2);
+  struct Cursor {
+    const uint8_t* at[MATS][2];
+    int k;
+    __device__ __forceinline__ void start(const StreamParams& p, int tile, int step, int lane) {
+      k = step * kStepK + (lane & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      const int k = step * kStepK + i * 32 + (lane & 3) * 8;
-      const int left = min(max(p.K - k, 0), 8) * 2;
+      for (int a = 0; a < MATS; ++a)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t row = n + 8 * h;
-        const bool in = row < p.N && left > 0;
-        const uint8_t* src = p.W[mat] + (in ? (row * p.ldw[mat] + k) * 2 : 0);
-        cp_async16(dst + (uint32_t)(((i * 2 + h) * 32 + lane) * 16), src, in ? left : 0);
+        for (int h = 0; h < 2; ++h) {
+          const int64_t row = min(tile * 16 + (lane >> 2) + 8 * h, p.N - 1);
+          at[a][h] = p.W[a] + (row * p.ldw[a] + k) * 2;
+        }
+    }
+    __device__ __forceinline__ void advance(const StreamParams&) {
+      k += WARPS * kStepK;
+#pragma unroll
+      for (int a = 0; a < MATS; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) at[a][h] += WARPS * kStepK * 2;
+    }
+    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
+      // A row's end: the bytes past it are zeros, and never read.
+#pragma unroll
+      for (int i = 0; i < kHalves; ++i) {
+        const int bytes = min(max((p.K - k - 32 * i) * 2, 0), 16);
+#pragma unroll
+        for (int a = 0; a < MATS; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            cp_async16(dst + (uint32_t)(a * kBytes + ((i * 2 + h) * 32 + lane) * 16),
+                       bytes > 0 ? at[a][h] + 64 * i : p.W[a], bytes);
       }
     }
-  }
-  static __device__ __forceinline__ Extra extra(const StreamParams&, int, int, int, int) { return {}; }
+  };
 
-  template <int TILES, int NT>
-  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT],
-                                                  const bool (&in)[NT], int step, uint32_t src, int lane,
-                                                  const Extra (&)[TILES], float (&sum)[TILES][NT][4]) {
+
+  template <int NT>
+  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
+                                                  uint32_t src, int lane,
+                                                  float (&sum)[MATS][NT][4]) {
+    uint4 x[kHalves][NT];
+    const int k0 = step * kStepK + (lane & 3) * 8;
+    if (step * kStepK + kStepK <= p.K) {
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i) {
-      uint4 x[NT];
+      for (int i = 0; i < kHalves; ++i)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        x[t] = load_a8<true>(row[t], in[t], step * kStepK + i * 32 + (lane & 3) * 8, p.K);
+        for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
+    } else {
 #pragma unroll
-      for (int r = 0; r < TILES; ++r) {
-        const uint32_t at = src + (uint32_t)(r * kBytes + (i * 64 + lane) * 16);
+      for (int i = 0; i < kHalves; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[i][t] = load_a8(row[t], k0 + 32 * i, p.K);
+    }
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i)
+#pragma unroll
+      for (int a = 0; a < MATS; ++a) {
+        const uint32_t at = src + (uint32_t)(a * kBytes + (i * 64 + lane) * 16);
         const uint4 w0 = lds128(at), w1 = lds128(at + 512);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma16816<FP16>(sum[r][t], w0.x, w1.x, w0.y, w1.y, x[t].x, x[t].y);
-          mma16816<FP16>(sum[r][t], w0.z, w1.z, w0.w, w1.w, x[t].z, x[t].w);
+          mma16816<FP16>(sum[a][t], w0.x, w1.x, w0.y, w1.y, x[i][t].x, x[i][t].y);
+          mma16816<FP16>(sum[a][t], w0.z, w1.z, w0.w, w1.w, x[i][t].z, x[i][t].w);
         }
       }
-    }
   }
 };
 
-// 4-bit weights in blocks of 16 rows x 128 values, as packed.  A code becomes
-// a 16-bit float without arithmetic:
+// 4-bit weights in blocks of 16 rows x 128 values, as packed: 1024 bytes of
+// codes and then the block's scales and zero points, so that a block is one
+// run of memory.  (With the scales in a region of their own, loaded a step
+// ahead into registers, 1 x 65537 x 8192 took 73 us; without loading them 54.)
+// A code becomes a 16-bit float without arithmetic:
 //   fp16: the subnormal q 2^-24, so the sums are scaled by 2^24;
 //   bf16: 128 + q, the low bits of 128's fraction.
 // W = (q - z) s, so a group's sum is s (sum q a - z sum a), with 128 added
 // to z for bf16.  The sums of a come from one more MMA, by a matrix of ones,
 // and serve every row tile of the step.
-template <bool FP16_, int GROUP>
+template <bool FP16_, int GROUP, int MATS, int R, int WARPS>
 struct Packed4 {
   static constexpr bool FP16 = FP16_;
   static constexpr int kStepK = 128;
-  static constexpr int kBytes = 1024;
-  static constexpr int kGroups = 128 / GROUP;  // groups of a block
-  struct Extra {
-    uint32_t scale[kGroups];  // rows g (low) and g + 8
-    uint32_t zero[(kGroups + 1) / 2];  // two bytes a group
-  };
+  static constexpr int kGroups = 128 / GROUP;         // groups of a block
+  static constexpr int kBytes = 1024 + 48 * kGroups;  // ring bytes, with zero points
+  static constexpr int kTiles = MATS * R;
+  static constexpr bool kShared = true;  // the scales
 
-  static __device__ __forceinline__ void fetch(const StreamParams& p, int mat, int tile, int step, uint32_t dst,
-                                               int lane) {
-    const bool in = tile < p.row_tiles;
-    const uint8_t* src = p.W[mat] + (in ? ((int64_t)tile * p.steps + step) * 1024 + lane * 16 : 0);
-    cp_async16(dst + (uint32_t)(lane * 16), src, in ? 16 : 0);
-    cp_async16(dst + (uint32_t)(512 + lane * 16), src + (in ? 512 : 0), in ? 16 : 0);
-  }
-
-  static __device__ __forceinline__ Extra extra(const StreamParams& p, int mat, int tile, int step, int lane) {
-    Extra e{};
-    if (tile >= p.row_tiles) return e;
-    const int64_t at = (((int64_t)tile * p.steps + step) * 8 + (lane >> 2)) * kGroups * 2;  // first of the rows' scales
-    const uint8_t* s = p.W[mat] + p.scales + at * 2;
-    if constexpr (kGroups == 1) {
-      e.scale[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-    } else if constexpr (kGroups == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-      e.scale[0] = v.x, e.scale[1] = v.y;
-    } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
-      e.scale[0] = v.x, e.scale[1] = v.y, e.scale[2] = v.z, e.scale[3] = v.w;
+  struct Cursor {
+    int64_t at;  // byte offset of the first row tile's block, the same in every matrix
+    __device__ __forceinline__ void start(const StreamParams& p, int tile, int step, int lane) {
+      at = ((int64_t)tile * p.steps + step) * p.block_bytes + lane * 16;
     }
-    if (p.zeros != 0) {
-      const uint8_t* z = p.W[mat] + p.zeros + at;
-      if constexpr (kGroups == 1) {
-        e.zero[0] = __ldg(reinterpret_cast<const uint16_t*>(z));
-      } else if constexpr (kGroups == 2) {
-        e.zero[0] = __ldg(reinterpret_cast<const uint32_t*>(z));
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
-        e.zero[0] = v.x, e.zero[1] = v.y;
+    __device__ __forceinline__ void advance(const StreamParams& p) { at += WARPS * p.block_bytes; }
+    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
+#pragma unroll
+      for (int a = 0; a < MATS; ++a) {
+        const uint8_t* src = p.W[a] + at;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t to = dst + (uint32_t)((a * R + r) * kBytes + lane * 16);
+          cp_async16(to, src, 16);
+          cp_async16(to + 512, src + 512, 16);
+          if (1024 + lane * 16 < p.block_bytes) cp_async16(to + 1024, src + 1024, 16);
+          if (r + 1 < R) src += (int64_t)p.steps * p.block_bytes;
+        }
       }
     }
-    return e;
-  }
+  };
 
-  template <int SHIFT>
-  static __device__ __forceinline__ uint32_t pair(uint32_t w) {
-    constexpr uint32_t magic = FP16 ? 0u : 0x43004300u;
-    return ((w >> SHIFT) & 0x000F000Fu) | magic;
+  // (w & 0x000F000F) | magic as one operation; magic is a register that the
+  // compiler cannot see through (two constants would make it two operations).
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t magic) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(magic));
+    return v;
   }
 
   static __device__ __forceinline__ float2 scales_of(uint32_t w, int scale_fp16) {
@@ -231,80 +258,95 @@ struct Packed4 {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
 
-  template <int TILES, int NT>
-  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT],
-                                                  const bool (&in)[NT], int step, uint32_t src, int lane,
-                                                  const Extra (&extra)[TILES], float (&sum)[TILES][NT][4]) {
+  template <int NT>
+  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
+                                                  uint32_t src, int lane,
+                                                  float (&sum)[kTiles][NT][4]) {
     constexpr uint32_t one = FP16 ? 0x3C003C00u : 0x3F803F80u;
+    uint32_t magic;
+    asm("mov.b32 %0, %1;" : "=r"(magic) : "n"(FP16 ? 0u : 0x43004300u));
     uint4 x[4][NT];
-    auto load_x = [&](int i) {
+    const int k0 = step * 128 + (lane & 3) * 8;
+    if (step * 128 + 128 <= p.K) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)  // K % 32 == 0: eight values are all inside or all outside
-        x[i][t] = load_a8<false>(row[t], in[t] && step * 128 + i * 32 < p.K, step * 128 + i * 32 + (lane & 3) * 8, p.K);
-    };
-    constexpr int kAhead = NT <= 2 ? 4 : 1;  // all of the step's A at once, or one quarter ahead (registers)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_x(i);
-    uint32_t q[TILES][2][4];
+        for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
+    } else {  // K % 32 == 0: eight values are all inside or all outside
 #pragma unroll
-    for (int r = 0; r < TILES; ++r)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 v = lds128(src + (uint32_t)(r * kBytes + h * 512 + lane * 16));
-        q[r][h][0] = v.x, q[r][h][1] = v.y, q[r][h][2] = v.z, q[r][h][3] = v.w;
+        for (int t = 0; t < NT; ++t)
+          x[i][t] = step * 128 + 32 * i < p.K ? __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i))
+                                              : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // the sums of A by group: every row of the product with ones is the same
+    float sa[kGroups][NT][2];
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
+          mma16816<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
+          mma16816<FP16>(d, one, one, one, one, x[i][t].z, x[i][t].w);
+        }
+        sa[j][t][0] = d[0];
+        sa[j][t][1] = d[1];
       }
-    float acc[TILES][NT][4], sa[NT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i + kAhead < 4) load_x(i + kAhead);
-      if (i % (GROUP / 32) == 0) {
+    for (int r = 0; r < kTiles; ++r) {
+      const uint4 q0 = lds128(src + (uint32_t)(r * kBytes + lane * 16));
+      const uint4 q1 = lds128(src + (uint32_t)(r * kBytes + 512 + lane * 16));
+      const uint32_t lo[4] = {q0.x, q0.y, q0.z, q0.w}, hi[4] = {q1.x, q1.y, q1.z, q1.w};
+      uint32_t sw[kGroups], zw[(kGroups + 1) / 2];  // rows g and g + 8: two scales, two zero points a group
+      const uint32_t at = src + (uint32_t)(r * kBytes + 1024 + (lane >> 2) * (kGroups * 4));
+      lds_words(at, sw);
+      if (p.has_zeros) {
+        const uint32_t az = src + (uint32_t)(r * kBytes + 1024 + kGroups * 32 + (lane >> 2) * (kGroups * 2));
+        if constexpr (kGroups == 1)
+          zw[0] = lds_u16(az);
+        else
+          lds_words(az, zw);
+      }
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        float acc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+#pragma unroll
+        for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
+          const uint32_t w0 = lo[i], w1 = hi[i];
+          const uint32_t a0 = pair(w0, magic), a1 = pair(w1, magic);
+          const uint32_t a2 = pair(w0 >> 4, magic), a3 = pair(w1 >> 4, magic);
+          const uint32_t b0 = pair(w0 >> 8, magic), b1 = pair(w1 >> 8, magic);
+          const uint32_t b2 = pair(w0 >> 12, magic), b3 = pair(w1 >> 12, magic);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816<FP16>(acc[t], a0, a1, a2, a3, x[i][t].x, x[i][t].y);
+            mma16816<FP16>(acc[t], b0, b1, b2, b3, x[i][t].z, x[i][t].w);
+          }
+        }
+        const float2 s = scales_of(sw[j], p.scale_fp16);
+        float z0 = 8.0f, z1 = 8.0f;
+        if (p.has_zeros) {
+          const uint32_t z = zw[j / 2] >> (16 * (j & 1));
+          z0 = (float)(z & 0xFFu);
+          z1 = (float)((z >> 8) & 0xFFu);
+        }
+        if (!FP16) z0 += 128.0f, z1 += 128.0f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sa[t][e] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < TILES; ++r) acc[r][t][e] = 0.0f;
+            const float zz = e < 2 ? z0 : z1, ss = e < 2 ? s.x : s.y;
+            const float v = FP16 ? fmaf(acc[t][e], 16777216.0f, -zz * sa[j][t][e & 1])
+                                 : fmaf(-zz, sa[j][t][e & 1], acc[t][e]);
+            sum[r][t][e] = fmaf(ss, v, sum[r][t][e]);
           }
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mma16816<FP16>(sa[t], one, one, one, one, x[i][t].x, x[i][t].y);
-        mma16816<FP16>(sa[t], one, one, one, one, x[i][t].z, x[i][t].w);
-      }
-#pragma unroll
-      for (int r = 0; r < TILES; ++r) {
-        const uint32_t w0 = q[r][0][i], w1 = q[r][1][i];
-        const uint32_t a0 = pair<0>(w0), a1 = pair<0>(w1), a2 = pair<4>(w0), a3 = pair<4>(w1);
-        const uint32_t b0 = pair<8>(w0), b1 = pair<8>(w1), b2 = pair<12>(w0), b3 = pair<12>(w1);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          mma16816<FP16>(acc[r][t], a0, a1, a2, a3, x[i][t].x, x[i][t].y);
-          mma16816<FP16>(acc[r][t], b0, b1, b2, b3, x[i][t].z, x[i][t].w);
-        }
-      }
-      if ((i + 1) % (GROUP / 32) == 0) {
-        const int j = i / (GROUP / 32);
-#pragma unroll
-        for (int r = 0; r < TILES; ++r) {
-          const float2 s = scales_of(extra[r].scale[j], p.scale_fp16);
-          float z0 = 8.0f, z1 = 8.0f;
-          if (p.zeros != 0) {
-            const uint32_t z = extra[r].zero[j / 2] >> (16 * (j & 1));
-            z0 = (float)(z & 0xFFu);
-            z1 = (float)((z >> 8) & 0xFFu);
-          }
-          if (!FP16) z0 += 128.0f, z1 += 128.0f;
-          constexpr float unit = FP16 ? 16777216.0f : 1.0f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float zz = e < 2 ? z0 : z1, ss = e < 2 ? s.x : s.y;
-              const float v = FP16 ? fmaf(acc[r][t][e], unit, -zz * sa[t][e & 1]) : fmaf(-zz, sa[t][e & 1], acc[r][t][e]);
-              sum[r][t][e] = fmaf(ss, v, sum[r][t][e]);
-            }
-        }
       }
     }
   }
@@ -312,52 +354,45 @@ struct Packed4 {
 
 // ---------------------------------------------------------------- kernel
 
-template <class P, int MATS, int R, int NT, int STAGES>
+template <class P, int TILES, int NT, int STAGES, int WARPS>
 struct StreamCfg {
-  static constexpr int kTiles = MATS * R;
-  static constexpr int kRowPitch = kTiles * 16 + 4;  // +4: a warp's fragment stores hit distinct banks
-  static constexpr int kStepBytes = kTiles * P::kBytes;
-  static constexpr int smem(int warps) {
-    return warps * STAGES * kStepBytes + warps * 8 * NT * kRowPitch * 4;
-  }
+  static constexpr int kRowPitch = TILES * 16 + 4;  // +4: a warp's fragment stores hit distinct banks
+  static constexpr int kStepBytes = TILES * P::kBytes;
+  static constexpr int kRing = WARPS * STAGES * kStepBytes;
+  static constexpr int kSmem = kRing + WARPS * 8 * NT * kRowPitch * 4;
 };
 
-// BLOCKS: blocks that share an SM.
+// P: the weights' policy.  MATS matrices, R row tiles of each a step, 8 * NT
+// rows of A, STAGES steps of the ring, WARPS a block, BLOCKS blocks an SM.
 template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS>
-__global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(StreamParams p) {
-  using C = StreamCfg<P, MATS, R, NT, STAGES>;
-  constexpr int TILES = C::kTiles;
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr int TILES = MATS * R;
+  using C = StreamCfg<P, TILES, NT, STAGES, WARPS>;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* red = reinterpret_cast<float*>(smem + WARPS * STAGES * C::kStepBytes);
+  float* red = reinterpret_cast<float*>(smem + C::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * C::kStepBytes);
+  const int grid = (int)gridDim.x;
 
   // The load cursor runs STAGES - 1 steps ahead of the compute cursor, across items.
-  int l_item = (int)blockIdx.x, l_tile = l_item % p.groups * R;
-  int l_step = warp, l_slot = 0;
-  const bool works = warp < p.steps;
+  int l_item = (int)blockIdx.x, l_step = warp, l_slot = 0;
+  if (warp >= p.steps) l_item = p.items;  // nothing for this warp
+  typename P::Cursor cursor;
+  if (l_item < p.items) cursor.start(p, l_item % p.groups * R, warp, lane);
   auto fetch_next = [&]() {
-    if (works && l_item < p.items) {
-#pragma unroll
-      for (int a = 0; a < MATS; ++a)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          P::fetch(p, a, l_tile + r, l_step, ring + (uint32_t)(l_slot * C::kStepBytes + (a * R + r) * P::kBytes), lane);
+    if (l_item < p.items) {
+      cursor.fetch(p, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
       l_step += WARPS;
-      if (l_step >= p.steps) {
+      if (l_step < p.steps) {
+        cursor.advance(p);
+      } else {
         l_step = warp;
-        l_item += (int)gridDim.x;
-        l_tile = l_item % p.groups * R;
+        l_item += grid;
+        if (l_item < p.items) cursor.start(p, l_item % p.groups * R, warp, lane);
       }
       if (++l_slot == STAGES) l_slot = 0;
     }
     cp_async_commit();
-  };
-  auto extras = [&](int tile, int step, typename P::Extra (&e)[TILES]) {
-#pragma unroll
-    for (int a = 0; a < MATS; ++a)
-#pragma unroll
-      for (int r = 0; r < R; ++r) e[a * R + r] = P::extra(p, a, tile + r, step, lane);
   };
 
   if (!p.b_constant) {
@@ -366,28 +401,18 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(StreamParams
   }
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) fetch_next();
-  typename P::Extra ahead[TILES];
-  const int l_first = (int)blockIdx.x % p.groups * R;
-  if (works && (int)blockIdx.x < p.items) extras(l_first, warp, ahead);
   if (p.b_constant) {  // the weights are on their way; A may be the previous kernel's output
     pdl_launch_dependents();
     pdl_wait();
   }
 
   int slot = 0;
-  for (int item = (int)blockIdx.x; item < p.items; item += (int)gridDim.x) {
+  for (int item = (int)blockIdx.x; item < p.items; item += grid) {
     const int group = item % p.groups;
     const int m0 = item / p.groups * (8 * NT);
-    const int next_item = item + (int)gridDim.x;
-    const int next_tile = next_item < p.items ? next_item % p.groups * R : -1;
-    const uint16_t* row[NT];
-    bool in[NT];
+    const uint16_t* row[NT];  // rows past M repeat the last: their sums are not stored
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int m = m0 + t * 8 + (lane >> 2);
-      in[t] = m < p.M;
-      row[t] = p.A + (int64_t)(in[t] ? m : 0) * p.lda;
-    }
+    for (int t = 0; t < NT; ++t) row[t] = p.A + (int64_t)min(m0 + t * 8 + (lane >> 2), p.M - 1) * p.lda;
     float sum[TILES][NT][4];
 #pragma unroll
     for (int r = 0; r < TILES; ++r)
@@ -397,14 +422,9 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(StreamParams
         for (int e = 0; e < 4; ++e) sum[r][t][e] = 0.0f;
 
     for (int step = warp; step < p.steps; step += WARPS) {
-      typename P::Extra now[TILES];
-#pragma unroll
-      for (int r = 0; r < TILES; ++r) now[r] = ahead[r];
-      const bool last = step + WARPS >= p.steps;
-      const int tile = last ? next_tile : group * R;
-      if (tile >= 0) extras(tile, last ? warp : step + WARPS, ahead);
       cp_async_wait<STAGES - 2>();
-      P::template multiply<TILES, NT>(p, row, in, step, ring + (uint32_t)(slot * C::kStepBytes), lane, now, sum);
+      if (P::kShared) __syncwarp();  // every lane's bytes are there, and the slot fetched into below has been read
+      P::template multiply<NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, sum);
       fetch_next();  // into the slot that the step before this one read
       if (++slot == STAGES) slot = 0;
     }
@@ -442,10 +462,10 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(StreamParams
 
 template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS>
 int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
-  using C = StreamCfg<P, MATS, R, NT, STAGES>;
+  using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS>;
   auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS>;
   static std::atomic<bool> attr_set[64];
-  if (const int rc = smem_attr_once(attr_set, kern, C::smem(WARPS)); rc != GP_OK) return rc;
+  if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
   p.groups = (p.row_tiles + R - 1) / R;
   const int64_t items = p.groups * (((int64_t)p.M + 8 * NT - 1) / (8 * NT));
   if (items > 0x40000000) return GP_ERR_SHAPE;  // more outputs than the memory holds
@@ -454,7 +474,7 @@ int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.items < slots ? p.items : slots));
   cfg.blockDim = dim3(32 * WARPS);
-  cfg.dynamicSmemBytes = C::smem(WARPS);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

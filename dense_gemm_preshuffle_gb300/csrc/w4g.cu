@@ -14,13 +14,13 @@ int w4g_run_launch(const W4gArgs& a, const HostContext& ctx, cudaStream_t stream
   p.W[1] = a.U;
   p.C = static_cast<uint16_t*>(a.C);
   p.ldc = a.ldc;
-  p.scales = l.scales;
-  p.zeros = a.has_zeros ? l.zeros : 0;
+  p.block_bytes = (int)l.block_bytes;
+  p.has_zeros = a.has_zeros ? 1 : 0;
   p.M = (int)a.M;
   p.N = (int)a.N;
   p.K = (int)a.K;
   p.steps = (int)l.kblocks;
-  p.row_tiles = (int)l.row_tiles;
+  p.row_tiles = (int)((a.N + 15) / 16);
   p.act = a.act;
   p.scale_fp16 = a.scale_fp16 ? 1 : 0;
   p.b_constant = a.b_constant ? 1 : 0;

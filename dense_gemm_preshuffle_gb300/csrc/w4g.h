@@ -7,9 +7,18 @@ namespace gp {
 
 struct StreamParams;
 
-// Two row tiles of 16 a warp step, from the width on at which every
-// resident block still gets several of them; else one.
-inline bool w4g_two_tiles(int64_t row_tiles, int num_sms) { return row_tiles >= 8 * (int64_t)num_sms; }
+// Row tiles of 16 of a step (1, 2 or 4, at most `most`): what leaves the
+// fewest row tiles to the block with most of them, where `slots` blocks are
+// resident, and of equals the largest, whose steps share A's loads and sums.
+inline int w4g_tiles_a_step(int row_tiles, int slots, int most) {
+  int best = 1, fewest = 0x7fffffff;
+  for (int r = 1; r <= most; r *= 2) {
+    const int groups = (row_tiles + r - 1) / r;
+    const int load = (groups + slots - 1) / slots * r;
+    if (load <= fewest) best = r, fewest = load;
+  }
+  return best;
+}
 
 int w4g_launch_32(const StreamParams& p, bool fp16, bool gated, int num_sms, cudaStream_t stream);
 int w4g_launch_64(const StreamParams& p, bool fp16, bool gated, int num_sms, cudaStream_t stream);

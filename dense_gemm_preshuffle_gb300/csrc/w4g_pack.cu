@@ -7,30 +7,29 @@ namespace gp {
 
 W4gLayout w4g_layout(int64_t N, int64_t K, int group, bool has_zeros) {
   W4gLayout l{};
-  l.row_tiles = (N + 15) / 16;
+  l.row_tiles = (N + 63) / 64 * 4;
   l.kblocks = (K + 127) / 128;
-  const int64_t blocks = l.row_tiles * l.kblocks;
-  const int64_t groups = blocks * 16 * (128 / group);
-  l.scales = blocks * 1024;
-  l.zeros = l.scales + groups * 2;
-  l.bytes = l.zeros + (has_zeros ? groups : 0);
+  l.block_bytes = 1024 + (has_zeros ? 48 : 32) * (128 / group);
+  l.bytes = l.row_tiles * l.kblocks * l.block_bytes;
   return l;
 }
 
 namespace {
 
-// Where the 32-bit word `i` (block c) of row n sits, in words.
-__device__ __forceinline__ int64_t word_offset(int64_t n, int64_t c, int i, int t, int64_t kblocks) {
-  const int64_t block = (n >> 4) * kblocks + c;
-  const int h = (int)(n >> 3) & 1, g = (int)n & 7;
-  return block * 256 + (h * 32 + 4 * g + t) * 4 + i;
+__device__ __forceinline__ int64_t block_at(int64_t n, int64_t c, const W4gLayout& l) {
+  return ((n >> 4) * l.kblocks + c) * l.block_bytes;
 }
 
-// Where the scale of row n, group j sits.
-__device__ __forceinline__ int64_t scale_offset(int64_t n, int64_t j, int gpb, int64_t kblocks) {
-  const int64_t block = (n >> 4) * kblocks + j / gpb;
+// Where the 32-bit word `w` of row n (its values 8w .. 8w + 7) sits, in bytes.
+__device__ __forceinline__ int64_t word_at(int64_t n, int64_t w, const W4gLayout& l) {
+  const int h = (int)(n >> 3) & 1, g = (int)n & 7, i = (int)(w >> 2) & 3, t = (int)w & 3;
+  return block_at(n, w >> 4, l) + (h * 32 + 4 * g + t) * 16 + 4 * i;
+}
+
+// Which of a block's scales (and zero points) row n's group j has.
+__device__ __forceinline__ int scale_in_block(int64_t n, int64_t j, int gpb) {
   const int h = (int)(n >> 3) & 1, g = (int)n & 7;
-  return ((block * 8 + g) * gpb + j % gpb) * 2 + h;
+  return (g * gpb + (int)(j % gpb)) * 2 + h;
 }
 
 // Eight codes k0..k7 in the low-nibble-first order of a row -> the packed
@@ -69,15 +68,14 @@ __global__ void w4g_pack_kernel(const uint32_t* codes, const uint16_t* scales, c
       const int64_t n = x / (l.kblocks * 16), w = x % (l.kblocks * 16);
       const bool in = n < N && w * 8 < K;
       const uint32_t v = in ? spread(codes[n * (K / 8) + w]) : 0u;
-      const int64_t c = w / 16;
-      const int in_block = (int)(w % 16);  // 32 i + 8 t = 8 in_block
-      reinterpret_cast<uint32_t*>(packed)[word_offset(n, c, in_block / 4, in_block % 4, l.kblocks)] = v;
+      *reinterpret_cast<uint32_t*>(packed + word_at(n, w, l)) = v;
     } else {
       const int64_t y = x - words, n = y / pgroups, j = y % pgroups;
       const bool in = n < N && j < groups;
-      const int64_t at = scale_offset(n, j, gpb, l.kblocks);
-      reinterpret_cast<uint16_t*>(packed + l.scales)[at] = in ? scales[n * groups + j] : (uint16_t)0;
-      if (zeros != nullptr) packed[l.zeros + at] = in ? zeros[n * groups + j] : (uint8_t)0;
+      uint8_t* block = packed + block_at(n, j / gpb, l) + 1024;
+      const int i = scale_in_block(n, j, gpb);
+      reinterpret_cast<uint16_t*>(block)[i] = in ? scales[n * groups + j] : (uint16_t)0;
+      if (zeros != nullptr) block[32 * gpb + i] = in ? zeros[n * groups + j] : (uint8_t)0;
     }
   }
 }
@@ -91,14 +89,13 @@ __global__ void w4g_unpack_kernel(const uint8_t* packed, int64_t N, int64_t K, i
   for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < words + N * groups; x += step) {
     if (x < words) {
       const int64_t n = x / (K / 8), w = x % (K / 8);
-      const int in_block = (int)(w % 16);
-      codes[x] = unspread(reinterpret_cast<const uint32_t*>(
-          packed)[word_offset(n, w / 16, in_block / 4, in_block % 4, l.kblocks)]);
+      codes[x] = unspread(*reinterpret_cast<const uint32_t*>(packed + word_at(n, w, l)));
     } else {
       const int64_t y = x - words, n = y / groups, j = y % groups;
-      const int64_t at = scale_offset(n, j, gpb, l.kblocks);
-      scales[y] = reinterpret_cast<const uint16_t*>(packed + l.scales)[at];
-      if (zeros != nullptr) zeros[y] = packed[l.zeros + at];
+      const uint8_t* block = packed + block_at(n, j / gpb, l) + 1024;
+      const int i = scale_in_block(n, j, gpb);
+      scales[y] = reinterpret_cast<const uint16_t*>(block)[i];
+      if (zeros != nullptr) zeros[y] = block[32 * gpb + i];
     }
   }
 }

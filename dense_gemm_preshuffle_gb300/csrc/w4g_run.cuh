@@ -7,15 +7,30 @@ namespace gp {
 
 namespace {
 
+template <bool FP16, int GROUP, int MATS, int R, int NT>
+int w4g_launch_r(const StreamParams& p, int num_sms, cudaStream_t stream) {
+  // 32 rows of A need the registers of a whole SM's two blocks.
+  constexpr int BLOCKS = NT == 4 ? 1 : 2;
+  constexpr int STAGES = (MATS * R == 4 ? 2 : 4) * (NT == 4 ? 2 : 1);
+  return launch_stream<Packed4<FP16, GROUP, MATS, R, 8>, MATS, R, NT, STAGES, 8, BLOCKS>(p, num_sms, stream);
+}
+
 template <bool FP16, int GROUP, int NT>
 int w4g_launch_nt(const StreamParams& p, bool gated, int num_sms, cudaStream_t stream) {
-  using P = Packed4<FP16, GROUP>;
-  // Two blocks an SM; 32 rows of A need more registers than that leaves for
-  // two row tiles, and take one block with a deeper ring.
-  constexpr int BLOCKS = NT == 4 ? 1 : 2, STAGES = NT == 4 ? 8 : 4;
-  if (gated) return launch_stream<P, 2, 1, NT, STAGES, 8, BLOCKS>(p, num_sms, stream);
-  if (w4g_two_tiles(p.row_tiles, num_sms)) return launch_stream<P, 1, 2, NT, STAGES, 8, BLOCKS>(p, num_sms, stream);
-  return launch_stream<P, 1, 1, NT, STAGES, 8, BLOCKS>(p, num_sms, stream);
+  // Four tiles a step fit the registers only beside 8 rows of A and few scales.
+  constexpr bool kFour = NT == 1 && GROUP >= 64;
+  const int slots = (NT == 4 ? 1 : 2) * num_sms;
+  if (gated) {
+    if constexpr (kFour)
+      if (w4g_tiles_a_step(p.row_tiles, slots, 2) == 2)
+        return w4g_launch_r<FP16, GROUP, 2, 2, NT>(p, num_sms, stream);
+    return w4g_launch_r<FP16, GROUP, 2, 1, NT>(p, num_sms, stream);
+  }
+  const int tiles = w4g_tiles_a_step(p.row_tiles, slots, kFour ? 4 : 2);
+  if constexpr (kFour)
+    if (tiles == 4) return w4g_launch_r<FP16, GROUP, 1, 4, NT>(p, num_sms, stream);
+  if (tiles == 2) return w4g_launch_r<FP16, GROUP, 1, 2, NT>(p, num_sms, stream);
+  return w4g_launch_r<FP16, GROUP, 1, 1, NT>(p, num_sms, stream);
 }
 
 template <bool FP16, int GROUP>

@@ -371,15 +371,15 @@ int gemm_packed_w4g_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t
  * zeros  : device, uint8 [N, ceil(K/group)] row-major, or NULL: 8 throughout.
  * packed : device, gemm_packed_w4g_bytes() bytes, written entirely.
  *
- * Layout: three regions, each cut into blocks of 16 rows x 128 K values
- * (block (r, c) at index r * ceil(K/128) + c; codes and scales past N or K
- * are 0):
- *   - codes, 1024 bytes a block: the 32-bit word i (0..3) of lane 4g + t and
- *     half h, at byte (h*32 + 4g + t)*16 + 4i, holds row 16r + 8h + g,
- *     k0 = 128c + 32i + 8t: codes k0..k0+7 at bits 0, 16, 4, 20, 8, 24, 12, 28.
- *   - scales: 16 * 128/group values a block; the one of row 8h + g, group j
- *     of the block, is at (g * 128/group + j)*2 + h.
- *   - zero points, where given: bytes in the scales' order.
+ * Layout: blocks of 16 rows x 128 K values, block (r, c) at index
+ * r * ceil(K/128) + c.  N is rounded up to 64; codes and scales past N or K
+ * are 0.  With e = 128/group, a block is 1024 + 32e bytes, or 1024 + 48e
+ * with zero points:
+ *   - codes, 1024 bytes: the 32-bit word i (0..3) of lane 4g + t and half h,
+ *     at byte (h*32 + 4g + t)*16 + 4i, holds row 16r + 8h + g, values k0 =
+ *     128c + 32i + 8t and on: codes k0..k0+7 at bits 0, 16, 4, 20, 8, 24, 12, 28.
+ *   - scales, 16e values: row 8h + g, group j of the block, at (g*e + j)*2 + h.
+ *   - zero points, 16e bytes, where given: in the scales' order.
  * One kernel on `stream`.
  */
 int gemm_preshuffle_w4g(const void* codes, const void* scales, const void* zeros, int64_t N, int64_t K, int group,

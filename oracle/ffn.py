@@ -172,23 +172,21 @@ def w4g_pack(codes: np.ndarray, scales_bits: np.ndarray, zeros: Optional[np.ndar
     """The packed buffer, element by element from the documented layout."""
     N, K = codes.shape[0], codes.shape[1] * 2
     q = w4g_codes(codes)
-    kb, rt, gpb = -(-K // 128), -(-N // 16), 128 // group
-    words = np.zeros(rt * kb * 256, dtype=np.uint32)
-    sc = np.zeros(rt * kb * gpb * 16, dtype=np.uint16)
-    zp = np.zeros(rt * kb * gpb * 16, dtype=np.uint8)
+    kb, rt, gpb = -(-K // 128), -(-N // 64) * 4, 128 // group
+    size = 1024 + (32 if zeros is None else 48) * gpb
+    out = np.zeros((rt * kb, size), dtype=np.uint8)
     place = [0, 16, 4, 20, 8, 24, 12, 28]
     for n in range(N):
         r, h, g = n // 16, n // 8 % 2, n % 8
         for k0 in range(0, K, 8):
             c, i, t = k0 // 128, k0 % 128 // 32, k0 % 32 // 8
-            w = 0
-            for e in range(8):
-                w |= int(q[n, k0 + e]) << place[e]
-            words[(r * kb + c) * 256 + (h * 32 + 4 * g + t) * 4 + i] = w
+            w = sum(int(q[n, k0 + e]) << place[e] for e in range(8))
+            at = (h * 32 + 4 * g + t) * 16 + 4 * i
+            out[r * kb + c, at:at + 4] = np.frombuffer(w.to_bytes(4, "little"), dtype=np.uint8)
         for j in range(scales_bits.shape[1]):
-            at = (((r * kb + j // gpb) * 8 + g) * gpb + j % gpb) * 2 + h
-            sc[at] = scales_bits[n, j]
+            at = (g * gpb + j % gpb) * 2 + h
+            block = out[r * kb + j // gpb, 1024:]
+            block[2 * at:2 * at + 2] = np.frombuffer(int(scales_bits[n, j]).to_bytes(2, "little"), dtype=np.uint8)
             if zeros is not None:
-                zp[at] = zeros[n, j]
-    parts = [words.view(np.uint8), sc.view(np.uint8)] + ([zp] if zeros is not None else [])
-    return np.concatenate(parts)
+                block[32 * gpb + at] = zeros[n, j]
+    return out.reshape(-1)
