@@ -333,9 +333,10 @@ def _matrix(name: str, t, shape, dtype) -> int:
 
 def _new_rows(like, rows: int, cols: int):
     """An empty [rows, cols] matrix of like's type whose rows start on 16-byte boundaries."""
+    import torch
     if cols % 8 == 0:
-        return like.new_empty((rows, cols))
-    return like.new_empty((rows, (cols + 7) // 8 * 8))[:, :cols]
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+    return torch.empty((rows, (cols + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :cols]
 
 
 def _stream_for(t, stream) -> Optional[int]:
@@ -396,7 +397,7 @@ def gated_matmul_backward(A, W_gate, W_up, dH, act: str = "silu", need_dA: bool 
         dU = _new_rows(A, N, K) if dU is None else dU
     if workspace is None:
         import torch
-        workspace = A.new_empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8)
+        workspace = torch.empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=A.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous CUDA tensor is wanted")
     _check((_lib or load_library()).gemm_gated_backward(
@@ -460,10 +461,14 @@ def _run_w4g(A, W: W4Weights, U: Optional[W4Weights], act: int, out, stream, b_c
     M = A.shape[0]
     lda = _matrix("A", A, (M, K), t)
     if out is None:
-        out = A.new_empty((M, N))
+        import torch
+        out = torch.empty((M, N), dtype=t, device=A.device)
+        ldc = N
+    else:
+        ldc = _matrix("out", out, (M, N), t)
     _check((_lib or load_library()).gemm_run_w4g(
         A.data_ptr(), lda, dt, packed.data_ptr(), None if U is None else U.packed.data_ptr(), scale_dtype, has_zeros,
-        M, N, K, group, act, out.data_ptr(), _matrix("out", out, (M, N), t),
+        M, N, K, group, act, out.data_ptr(), ldc,
         GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, _stream_for(A, stream)), "gemm_run_w4g")
     return out
 

@@ -145,7 +145,7 @@ int map_parts(CUtensorMap* map, float* partial, int64_t slices, int64_t rows, in
 size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K) { return (size_t)workspace_of(M, N, K).bytes; }
 
 int gated_run_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
-  if (a.M <= kGatedStreamRows) return gated_stream_launch(a, ctx, stream);
+  if (gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)) return gated_stream_launch(a, a.H, nullptr, a.ldh, ctx, stream);
   return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, stream);
 }
 
@@ -154,7 +154,9 @@ int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const Matrix dg{ws, a.M, a.N, w.pitch}, du{ws + w.du, a.M, a.N, w.pitch};
   float* partial = reinterpret_cast<float*>(ws + w.partial);
-  int rc = products_launch(a, ctx, dg, du, stream);
+  int rc = gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)
+               ? gated_stream_launch(a, ws, ws + w.du, w.pitch, ctx, stream)
+               : products_launch(a, ctx, dg, du, stream);
   if (rc != GP_OK) return rc;
   if (a.dA != nullptr) {
     GatedMaps maps{};

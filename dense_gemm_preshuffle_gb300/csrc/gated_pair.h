@@ -41,8 +41,10 @@ int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p,
 int gated_add_parts_launch(const float* partial, int parts, int outputs, int64_t rows, int64_t cols, int64_t pitch,
                            void* out0, int64_t ld0, void* out1, int64_t ld1, bool fp16, int num_sms,
                            cudaStream_t stream);
-// The forward product for few tokens (gated_stream.cu): M <= 32 fills its MMAs.
-constexpr int64_t kGatedStreamRows = 32;
-int gated_stream_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream);
+// FORWARD and SLOPES for few tokens or little work (gated_stream.cu): whether
+// it takes them, and the launch, into out0 (and out1 for SLOPES) of pitch ld.
+bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms);
+int gated_stream_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
+                        cudaStream_t stream);
 
 }  // namespace gp

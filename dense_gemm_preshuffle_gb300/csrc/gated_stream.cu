@@ -1,5 +1,9 @@
 // The gated products for a few tokens: the streaming kernel over the rows of
 // G and U as they are.
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+
 #include "gated_pair.h"
 #include "stream.cuh"
 
@@ -7,21 +11,58 @@ namespace gp {
 
 namespace {
 
-template <bool FP16, int NT>
+constexpr int kHalves = 2;  // 128 contiguous bytes of a row a step: 64 cost a third of the bandwidth
+
+template <bool FP16, int NT, bool SLOPES, int WARPS, int BLOCKS>
 int launch_nt(const StreamParams& p, int num_sms, cudaStream_t stream) {
-  return launch_stream<Rows16<FP16, 2, 1, 8>, 2, 1, NT, 3, 8, 2>(p, num_sms, stream);
+  // three stages, or the two that fit beside 32 rows' sums
+  constexpr int kRed = WARPS * 8 * NT * 36 * 4, kStep = WARPS * 2 * kHalves * 1024;
+  constexpr int kFit = ((BLOCKS == 1 ? 227 : 113) * 1024 - kRed) / kStep, STAGES = kFit < 3 ? kFit : 3;
+  return launch_stream<Rows16<FP16, kHalves, 2, 1, WARPS>, 2, 1, NT, STAGES, WARPS, BLOCKS, SLOPES>(p, num_sms,
+                                                                                                   stream);
 }
 
-template <bool FP16>
+template <bool FP16, bool SLOPES>
 int launch_type(const StreamParams& p, int num_sms, cudaStream_t stream) {
-  if (p.M <= 8) return launch_nt<FP16, 1>(p, num_sms, stream);
-  if (p.M <= 16) return launch_nt<FP16, 2>(p, num_sms, stream);
-  return launch_nt<FP16, 4>(p, num_sms, stream);
+  // Few units: a block has an SM to itself, and twice the warps (1 x 1024 x
+  // 8192, 64 units: 9.6 us against 15.3 with 8 warps).
+  const bool few = (int64_t)p.row_tiles * ((p.M + 31) / 32) <= num_sms;
+  if (p.M <= 8)
+    return few ? launch_nt<FP16, 1, SLOPES, 16, 1>(p, num_sms, stream)
+               : launch_nt<FP16, 1, SLOPES, 8, 2>(p, num_sms, stream);
+  if (p.M <= 16)
+    return few ? launch_nt<FP16, 2, SLOPES, 16, 1>(p, num_sms, stream)
+               : launch_nt<FP16, 2, SLOPES, 8, 2>(p, num_sms, stream);
+  return few ? launch_nt<FP16, 4, SLOPES, 16, 1>(p, num_sms, stream)
+             : launch_nt<FP16, 4, SLOPES, 8, 2>(p, num_sms, stream);
 }
 
 }  // namespace
 
-int gated_stream_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
+bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms) {
+  static const int forced = [] {
+    const char* e = std::getenv("GP_GATED_STREAM");
+    return (e == nullptr || *e == '\0') ? -1 : std::atoi(e);
+  }();
+  if (forced >= 0) return forced != 0;
+  // Microseconds of each form by its measured rates, and the smaller.
+  // Streaming: a unit reads 16 rows of G and of U; the rate of a block falls
+  // with the rows of A beside them, and is higher where it has an SM alone.
+  const int64_t chunks = (M + 31) / 32, units = (N + 15) / 16 * chunks;
+  const int rows = M <= 8 ? 0 : M <= 16 ? 1 : 2;
+  constexpr double kAlone[3] = {73.0, 59.0, 36.0}, kShared[3] = {19.4, 17.0, 16.0};  // KB / us
+  const double kb = 0.064 * (double)K, share = (double)units / (2.0 * num_sms);
+  const double turns = share <= 1.0 ? 1.0 : chunks == 1 ? share : std::ceil(share);
+  const double stream_us = 3.0 + (units <= num_sms ? kb / kAlone[rows] : turns * kb / kShared[rows]);
+  // Tiles: 0.285 us for 64 values of K on every pair's tile, or the weights' reading.
+  const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128), pairs = num_sms / 2;
+  const double waves = (double)((tiles + pairs - 1) / pairs);
+  const double tile_us = std::max(4.5 + waves * 0.285 * (double)((K + 63) / 64), 6.0 + 4e-6 * (double)N * (double)K / 6.0);
+  return stream_us < tile_us;
+}
+
+int gated_stream_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
+                        cudaStream_t stream) {
   StreamParams p{};
   p.A = static_cast<const uint16_t*>(a.A);
   p.lda = a.lda;
@@ -29,17 +70,23 @@ int gated_stream_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t
   p.W[1] = static_cast<const uint8_t*>(a.U);
   p.ldw[0] = a.ldg;
   p.ldw[1] = a.ldu;
-  p.C = static_cast<uint16_t*>(a.H);
-  p.ldc = a.ldh;
+  p.C = static_cast<uint16_t*>(out0);
+  p.C2 = static_cast<uint16_t*>(out1);
+  p.ldc = ld;
+  p.dH = static_cast<const uint16_t*>(a.dH);
+  p.lddh = a.lddh;
   p.M = (int)a.M;
   p.N = (int)a.N;
   p.K = (int)a.K;
-  constexpr int kStepK = Rows16<false, 2, 1, 8>::kStepK;
-  p.steps = (int)((a.K + kStepK - 1) / kStepK);
+  p.steps = (int)((a.K + 32 * kHalves - 1) / (32 * kHalves));
   p.row_tiles = (int)((a.N + 15) / 16);
   p.act = a.act;
   p.b_constant = a.b_constant ? 1 : 0;
-  return a.fp16 ? launch_type<true>(p, ctx.num_sms, stream) : launch_type<false>(p, ctx.num_sms, stream);
+  if (a.dH != nullptr)
+    return a.fp16 ? launch_type<true, true>(p, ctx.num_sms, stream)
+                  : launch_type<false, true>(p, ctx.num_sms, stream);
+  return a.fp16 ? launch_type<true, false>(p, ctx.num_sms, stream)
+                : launch_type<false, false>(p, ctx.num_sms, stream);
 }
 
 }  // namespace gp

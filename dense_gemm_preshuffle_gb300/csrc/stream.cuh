@@ -15,8 +15,9 @@
 //     for both: lane t of a row's four takes 8 consecutive values, which are
 //     the values 2t, 2t+1, 2t+8, 2t+9 of two MMAs.  The sum does not change.
 //   - The warps of a block take a row tile's steps in turn; their sums meet in
-//     shared memory in a fixed order.  Blocks are persistent over the tiles,
-//     and the loads of the next tile are in flight while one is summed.
+//     shared memory in a fixed order.  Each block has a run of row tiles, one
+//     more or less than any other, and the loads of the next tiles are in
+//     flight while some are summed.
 //   - A is read through L1, which keeps it from tile to tile.
 // mma.sync, not tcgen05: at M <= 32 the arithmetic is a few percent of
 // either's rate, and register fragments spare the weights two trips through
@@ -43,8 +44,11 @@ struct StreamParams {
   int M, N, K;
   int steps;                 // steps of a row tile
   int row_tiles;             // ceil(N / 16)
-  int groups;                // ceil(row_tiles / R): a block's unit of rows
-  int items;                 // groups * chunks of 8 * NT rows of A
+  int units;                 // row_tiles * chunks of 8 * NT rows of A
+  int keep_sums;             // 4 bits: room for A's sums in shared memory
+  const uint16_t* dH;        // slopes: [M, N]; C is then dg and C2 du
+  int64_t lddh;
+  uint16_t* C2;
   int act;
   int scale_fp16;
   int b_constant;
@@ -108,12 +112,17 @@ __device__ __forceinline__ uint4 load_a8(const uint16_t* row, int k, int K) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float act_of(float v, int act) {
+__device__ __forceinline__ ActSlope act_of(float v, int act) {
   switch (act) {
-    case GP_ACT_RELU: return act_value<GP_ACT_RELU>(v);
-    case GP_ACT_SILU: return act_value<GP_ACT_SILU>(v);
-    default: return act_value<GP_ACT_GELU>(v);
+    case GP_ACT_RELU: return act_slope<GP_ACT_RELU>(v);
+    case GP_ACT_SILU: return act_slope<GP_ACT_SILU>(v);
+    default: return act_slope<GP_ACT_GELU>(v);
   }
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint16_t round16(float v) {
+  return FP16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // ---------------------------------------------------------------- weights
@@ -126,79 +135,87 @@ __device__ __forceinline__ float act_of(float v, int act) {
 // as row N - 1, packed weights are padded, and neither's sums are stored.
 
 // 16-bit rows as the caller has them: rows g and g + 8 of a tile, 16 bytes a
-// lane and 32 values.
-template <bool FP16_, int MATS, int R, int WARPS>
+// lane and 32 values; HALVES of those a step (2: 128 contiguous bytes of a row).
+template <bool FP16_, int HALVES, int MATS, int R, int WARPS>
 struct Rows16 {
-  static_assert(R == 1, "one row tile of each matrix");
   static constexpr bool FP16 = FP16_;
-  static constexpr int kHalves = 2;  // 128 contiguous bytes of a row
-  static constexpr int kStepK = 32 * kHalves;
-  static constexpr int kBytes = 1024 * kHalves;
+  static constexpr int kStepK = 32 * HALVES;
+  static constexpr int kBytes = 1024 * HALVES;
   static constexpr bool kShared = false;
+  static constexpr int kSums = 0;
 
   struct Cursor {
-    const uint8_t* at[MATS][2];
+    const uint8_t* at[MATS][R][2];
     int k;
     __device__ __forceinline__ void start(const StreamParams& p, int tile, int step, int lane) {
       k = step * kStepK + (lane & 3) * 8;
 #pragma unroll
       for (int a = 0; a < MATS; ++a)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t row = min(tile * 16 + (lane >> 2) + 8 * h, p.N - 1);
-          at[a][h] = p.W[a] + (row * p.ldw[a] + k) * 2;
-        }
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t row = min((int64_t)(tile + r) * 16 + (lane >> 2) + 8 * h, (int64_t)p.N - 1);
+            at[a][r][h] = p.W[a] + (row * p.ldw[a] + k) * 2;
+          }
     }
     __device__ __forceinline__ void advance(const StreamParams&) {
       k += WARPS * kStepK;
 #pragma unroll
       for (int a = 0; a < MATS; ++a)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) at[a][h] += WARPS * kStepK * 2;
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) at[a][r][h] += WARPS * kStepK * 2;
     }
-    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
+    __device__ __forceinline__ void fetch(const StreamParams& p, int tiles, uint32_t dst, int lane) const {
       // A row's end: the bytes past it are zeros, and never read.
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i) {
+      for (int i = 0; i < HALVES; ++i) {
         const int bytes = min(max((p.K - k - 32 * i) * 2, 0), 16);
 #pragma unroll
         for (int a = 0; a < MATS; ++a)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            cp_async16(dst + (uint32_t)(a * kBytes + ((i * 2 + h) * 32 + lane) * 16),
-                       bytes > 0 ? at[a][h] + 64 * i : p.W[a], bytes);
+          for (int r = 0; r < R; ++r) {
+            if (r >= tiles) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              cp_async16(dst + (uint32_t)((a * R + r) * kBytes + ((i * 2 + h) * 32 + lane) * 16),
+                         bytes > 0 ? at[a][r][h] + 64 * i : p.W[a], bytes);
+          }
       }
     }
   };
 
-
-  template <int NT>
+  // The first N row tiles of each matrix.
+  template <int N, int NT>
   static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
-                                                  uint32_t src, int lane,
-                                                  float (&sum)[MATS][NT][4]) {
-    uint4 x[kHalves][NT];
+                                                  uint32_t src, int lane, float*, bool,
+                                                  float (&sum)[MATS * R][NT][4]) {
+    uint4 x[HALVES][NT];
     const int k0 = step * kStepK + (lane & 3) * 8;
     if (step * kStepK + kStepK <= p.K) {
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i)
+      for (int i = 0; i < HALVES; ++i)
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
     } else {
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i)
+      for (int i = 0; i < HALVES; ++i)
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[i][t] = load_a8(row[t], k0 + 32 * i, p.K);
     }
 #pragma unroll
-    for (int i = 0; i < kHalves; ++i)
+    for (int i = 0; i < HALVES; ++i)
 #pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        const uint32_t at = src + (uint32_t)(a * kBytes + (i * 64 + lane) * 16);
+      for (int r = 0; r < MATS * R; ++r) {
+        if (r % R >= N) continue;
+        const uint32_t at = src + (uint32_t)(r * kBytes + (i * 64 + lane) * 16);
         const uint4 w0 = lds128(at), w1 = lds128(at + 512);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma16816<FP16>(sum[a][t], w0.x, w1.x, w0.y, w1.y, x[i][t].x, x[i][t].y);
-          mma16816<FP16>(sum[a][t], w0.z, w1.z, w0.w, w1.w, x[i][t].z, x[i][t].w);
+          mma16816<FP16>(sum[r][t], w0.x, w1.x, w0.y, w1.y, x[i][t].x, x[i][t].y);
+          mma16816<FP16>(sum[r][t], w0.z, w1.z, w0.w, w1.w, x[i][t].z, x[i][t].w);
         }
       }
   }
@@ -212,8 +229,9 @@ struct Rows16 {
 //   fp16: the subnormal q 2^-24, so the sums are scaled by 2^24;
 //   bf16: 128 + q, the low bits of 128's fraction.
 // W = (q - z) s, so a group's sum is s (sum q a - z sum a), with 128 added
-// to z for bf16.  The sums of a come from one more MMA, by a matrix of ones,
-// and serve every row tile of the step.
+// to z for bf16.  The sums of a come from one more MMA, by a matrix of ones.
+// They serve every row tile of the step, and, kept in shared memory, the
+// later steps with the same values of A, which the same warp takes.
 template <bool FP16_, int GROUP, int MATS, int R, int WARPS>
 struct Packed4 {
   static constexpr bool FP16 = FP16_;
@@ -222,6 +240,7 @@ struct Packed4 {
   static constexpr int kBytes = 1024 + 48 * kGroups;  // ring bytes, with zero points
   static constexpr int kTiles = MATS * R;
   static constexpr bool kShared = true;  // the scales
+  static constexpr int kSums = kGroups;  // sums of A that a step keeps for each of its rows
 
   struct Cursor {
     int64_t at;  // byte offset of the first row tile's block, the same in every matrix
@@ -229,12 +248,13 @@ struct Packed4 {
       at = ((int64_t)tile * p.steps + step) * p.block_bytes + lane * 16;
     }
     __device__ __forceinline__ void advance(const StreamParams& p) { at += WARPS * p.block_bytes; }
-    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
+    __device__ __forceinline__ void fetch(const StreamParams& p, int tiles, uint32_t dst, int lane) const {
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
         const uint8_t* src = p.W[a] + at;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+          if (r >= tiles) break;
           const uint32_t to = dst + (uint32_t)((a * R + r) * kBytes + lane * 16);
           cp_async16(to, src, 16);
           cp_async16(to + 512, src + 512, 16);
@@ -258,9 +278,10 @@ struct Packed4 {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
 
-  template <int NT>
+  // The first N row tiles of each matrix.
+  template <int N, int NT>
   static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
-                                                  uint32_t src, int lane,
+                                                  uint32_t src, int lane, float* kept, bool have,
                                                   float (&sum)[kTiles][NT][4]) {
     constexpr uint32_t one = FP16 ? 0x3C003C00u : 0x3F803F80u;
     uint32_t magic;
@@ -281,22 +302,31 @@ struct Packed4 {
                                               : make_uint4(0u, 0u, 0u, 0u);
     }
     // the sums of A by group: every row of the product with ones is the same
-    float sa[kGroups][NT][2];
+    float2 sa[kGroups][NT];
+    if (have) {
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j)
+      for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < NT; ++t)
+          sa[j][t] = *reinterpret_cast<const float2*>(kept + (j * NT + t) * 8 + 2 * (lane & 3));
+    } else {
 #pragma unroll
-        for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
-          mma16816<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
-          mma16816<FP16>(d, one, one, one, one, x[i][t].z, x[i][t].w);
+      for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
+            mma16816<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
+            mma16816<FP16>(d, one, one, one, one, x[i][t].z, x[i][t].w);
+          }
+          sa[j][t] = make_float2(d[0], d[1]);
+          if (kept != nullptr && lane < 4) *reinterpret_cast<float2*>(kept + (j * NT + t) * 8 + 2 * lane) = sa[j][t];
         }
-        sa[j][t][0] = d[0];
-        sa[j][t][1] = d[1];
-      }
+    }
 #pragma unroll
     for (int r = 0; r < kTiles; ++r) {
+      if (r % R >= N) continue;
       const uint4 q0 = lds128(src + (uint32_t)(r * kBytes + lane * 16));
       const uint4 q1 = lds128(src + (uint32_t)(r * kBytes + 512 + lane * 16));
       const uint32_t lo[4] = {q0.x, q0.y, q0.z, q0.w}, hi[4] = {q1.x, q1.y, q1.z, q1.w};
@@ -342,9 +372,8 @@ struct Packed4 {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float zz = e < 2 ? z0 : z1, ss = e < 2 ? s.x : s.y;
-            const float v = FP16 ? fmaf(acc[t][e], 16777216.0f, -zz * sa[j][t][e & 1])
-                                 : fmaf(-zz, sa[j][t][e & 1], acc[t][e]);
+            const float zz = e < 2 ? z0 : z1, ss = e < 2 ? s.x : s.y, of_a = e & 1 ? sa[j][t].y : sa[j][t].x;
+            const float v = FP16 ? fmaf(acc[t][e], 16777216.0f, -zz * of_a) : fmaf(-zz, of_a, acc[t][e]);
             sum[r][t][e] = fmaf(ss, v, sum[r][t][e]);
           }
       }
@@ -362,33 +391,53 @@ struct StreamCfg {
   static constexpr int kSmem = kRing + WARPS * 8 * NT * kRowPitch * 4;
 };
 
-// P: the weights' policy.  MATS matrices, R row tiles of each a step, 8 * NT
+// P: the weights' policy.  MATS matrices, R (1 or 2) row tiles of each a step, 8 * NT
 // rows of A, STAGES steps of the ring, WARPS a block, BLOCKS blocks an SM.
-template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS>
+// SLOPES: dg and du of the gated product in place of it.
+template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES>
 __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid_constant__ StreamParams p) {
+  static_assert(R == 1 || R == 2, "a short step has one tile of each matrix");
   constexpr int TILES = MATS * R;
   using C = StreamCfg<P, TILES, NT, STAGES, WARPS>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem + C::kRing);
+  [[maybe_unused]] float* sums = reinterpret_cast<float*>(smem + C::kSmem);  // A's, by step, group and row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * C::kStepBytes);
-  const int grid = (int)gridDim.x;
+  // This block's run of (chunk of A's rows, row tile) units, one more or less
+  // than any other's; a step takes up to R row tiles of one chunk.
+  const int first = (int)((int64_t)p.units * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)p.units * (blockIdx.x + 1) / gridDim.x);
+  struct Place {
+    int chunk, tile, tiles;
+  };
+  auto place_of = [&](int unit) {
+    Place a;
+    a.chunk = unit / p.row_tiles;
+    a.tile = unit - a.chunk * p.row_tiles;
+    a.tiles = min(R, min(end - unit, p.row_tiles - a.tile));
+    return a;
+  };
 
-  // The load cursor runs STAGES - 1 steps ahead of the compute cursor, across items.
-  int l_item = (int)blockIdx.x, l_step = warp, l_slot = 0;
-  if (warp >= p.steps) l_item = p.items;  // nothing for this warp
+  // The load cursor runs STAGES - 1 steps ahead of the compute cursor, across units.
+  int l_unit = warp < p.steps ? first : end;  // else nothing for this warp
+  int l_step = warp, l_slot = 0;
+  Place l_place = place_of(first);
   typename P::Cursor cursor;
-  if (l_item < p.items) cursor.start(p, l_item % p.groups * R, warp, lane);
+  if (l_unit < end) cursor.start(p, l_place.tile, warp, lane);
   auto fetch_next = [&]() {
-    if (l_item < p.items) {
-      cursor.fetch(p, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
+    if (l_unit < end) {
+      cursor.fetch(p, l_place.tiles, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
       l_step += WARPS;
       if (l_step < p.steps) {
         cursor.advance(p);
       } else {
         l_step = warp;
-        l_item += grid;
-        if (l_item < p.items) cursor.start(p, l_item % p.groups * R, warp, lane);
+        l_unit += l_place.tiles;
+        if (l_unit < end) {
+          l_place = place_of(l_unit);
+          cursor.start(p, l_place.tile, warp, lane);
+        }
       }
       if (++l_slot == STAGES) l_slot = 0;
     }
@@ -406,10 +455,12 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     pdl_wait();
   }
 
-  int slot = 0;
-  for (int item = (int)blockIdx.x; item < p.items; item += grid) {
-    const int group = item % p.groups;
-    const int m0 = item / p.groups * (8 * NT);
+  int slot = 0, of_chunk = -1;
+  for (int unit = first; unit < end;) {
+    const Place at = place_of(unit);
+    const int m0 = at.chunk * (8 * NT);
+    const bool have = P::kSums > 0 && p.keep_sums && of_chunk == at.chunk;
+    of_chunk = at.chunk;
     const uint16_t* row[NT];  // rows past M repeat the last: their sums are not stored
 #pragma unroll
     for (int t = 0; t < NT; ++t) row[t] = p.A + (int64_t)min(m0 + t * 8 + (lane >> 2), p.M - 1) * p.lda;
@@ -424,7 +475,11 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     for (int step = warp; step < p.steps; step += WARPS) {
       cp_async_wait<STAGES - 2>();
       if (P::kShared) __syncwarp();  // every lane's bytes are there, and the slot fetched into below has been read
-      P::template multiply<NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, sum);
+      float* kept = P::kSums > 0 && p.keep_sums ? sums + step * (P::kSums * 8 * NT) : nullptr;
+      if (at.tiles == R)
+        P::template multiply<R, NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
+      else
+        P::template multiply<1, NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
       fetch_next();  // into the slot that the step before this one read
       if (++slot == STAGES) slot = 0;
     }
@@ -443,38 +498,50 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     const int used = min(WARPS, p.steps);  // warps past that hold zeros
     for (int x = threadIdx.x; x < live * R * 16; x += 32 * WARPS) {
       const int m = x / (R * 16), n = x % (R * 16);
+      const int64_t col = (int64_t)at.tile * 16 + n;
+      if (n >= at.tiles * 16 || col >= p.N) continue;
       float v[MATS];
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
         v[a] = 0.0f;
         for (int w = 0; w < used; ++w) v[a] += red[(w * 8 * NT + m) * C::kRowPitch + a * R * 16 + n];
       }
-      const float out = MATS == 2 ? act_of(v[0], p.act) * v[MATS - 1] : v[0];
-      const int64_t col = (int64_t)group * (R * 16) + n;
-      if (col < p.N)
-        p.C[(int64_t)(m0 + m) * p.ldc + col] = P::FP16 ? __half_as_ushort(__float2half_rn(out))
-                                                       : __bfloat16_as_ushort(__float2bfloat16_rn(out));
+      const int64_t to = (int64_t)(m0 + m) * p.ldc + col;
+      if constexpr (SLOPES) {
+        const uint16_t d16 = __ldg(p.dH + (int64_t)(m0 + m) * p.lddh + col);
+        const float d = P::FP16 ? __half2float(__ushort_as_half(d16)) : __bfloat162float(__ushort_as_bfloat16(d16));
+        const ActSlope s = act_of(v[0], p.act);
+        p.C[to] = round16<P::FP16>(d * v[MATS - 1] * s.slope);
+        p.C2[to] = round16<P::FP16>(d * s.value);
+      } else {
+        p.C[to] = round16<P::FP16>(MATS == 2 ? act_of(v[0], p.act).value * v[MATS - 1] : v[0]);
+      }
     }
-    __syncthreads();  // before the next item's sums replace these
+    __syncthreads();  // before the next unit's sums replace these
+    unit += at.tiles;
   }
   cp_async_wait<0>();
 }
 
-template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS>
+template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES = false>
 int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
   using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS>;
-  auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS>;
+  auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS, SLOPES>;
   static std::atomic<bool> attr_set[64];
-  if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
-  p.groups = (p.row_tiles + R - 1) / R;
-  const int64_t items = p.groups * (((int64_t)p.M + 8 * NT - 1) / (8 * NT));
-  if (items > 0x40000000) return GP_ERR_SHAPE;  // more outputs than the memory holds
-  p.items = (int)items;
+  constexpr int kRoom = (BLOCKS == 1 ? 227 : 113) * 1024;
+  static_assert(C::kSmem <= kRoom, "shared memory budget");
+  if (const int rc = smem_attr_once(attr_set, kern, P::kSums > 0 ? kRoom : C::kSmem); rc != GP_OK) return rc;
+  const int64_t units = p.row_tiles * (((int64_t)p.M + 8 * NT - 1) / (8 * NT));
+  if (units > 0x40000000) return GP_ERR_SHAPE;  // more outputs than the memory holds
+  p.units = (int)units;
+  // A's sums are kept where a block has several units and they fit.
   const int slots = BLOCKS * num_sms;
+  const int64_t sums = (int64_t)p.steps * P::kSums * 8 * NT * 4;
+  p.keep_sums = P::kSums > 0 && units > slots && C::kSmem + sums <= kRoom ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.items < slots ? p.items : slots));
+  cfg.gridDim = dim3((unsigned)(p.units < slots ? p.units : slots));
   cfg.blockDim = dim3(32 * WARPS);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = (size_t)(C::kSmem + (p.keep_sums ? sums : 0));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -17,20 +17,17 @@ int w4g_launch_r(const StreamParams& p, int num_sms, cudaStream_t stream) {
 
 template <bool FP16, int GROUP, int NT>
 int w4g_launch_nt(const StreamParams& p, bool gated, int num_sms, cudaStream_t stream) {
-  // Four tiles a step fit the registers only beside 8 rows of A and few scales.
-  constexpr bool kFour = NT == 1 && GROUP >= 64;
-  const int slots = (NT == 4 ? 1 : 2) * num_sms;
+  // Two tiles of each matrix a step share A's loads and sums; one where no
+  // block has two.  A pair of matrices with two tiles each fits the registers
+  // only beside 8 rows of A and few scales.
+  const bool two = p.row_tiles > (NT == 4 ? 1 : 2) * num_sms;
   if (gated) {
-    if constexpr (kFour)
-      if (w4g_tiles_a_step(p.row_tiles, slots, 2) == 2)
-        return w4g_launch_r<FP16, GROUP, 2, 2, NT>(p, num_sms, stream);
+    if constexpr (NT == 1 && GROUP >= 64)
+      if (two) return w4g_launch_r<FP16, GROUP, 2, 2, NT>(p, num_sms, stream);
     return w4g_launch_r<FP16, GROUP, 2, 1, NT>(p, num_sms, stream);
   }
-  const int tiles = w4g_tiles_a_step(p.row_tiles, slots, kFour ? 4 : 2);
-  if constexpr (kFour)
-    if (tiles == 4) return w4g_launch_r<FP16, GROUP, 1, 4, NT>(p, num_sms, stream);
-  if (tiles == 2) return w4g_launch_r<FP16, GROUP, 1, 2, NT>(p, num_sms, stream);
-  return w4g_launch_r<FP16, GROUP, 1, 1, NT>(p, num_sms, stream);
+  return two ? w4g_launch_r<FP16, GROUP, 1, 2, NT>(p, num_sms, stream)
+             : w4g_launch_r<FP16, GROUP, 1, 1, NT>(p, num_sms, stream);
 }
 
 template <bool FP16, int GROUP>
