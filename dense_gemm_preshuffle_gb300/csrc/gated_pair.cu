@@ -4,8 +4,9 @@
 //
 //   FORWARD  H  = act(A G^T) * (A U^T)
 //   SLOPES   dg = dH (A U^T) act'(A G^T),  du = dH act(A G^T)
-//   INPUT    dA = dg G + du U              (one sum over both halves)
-//   WEIGHTS  dG = dg^T A,  dU = du^T A     (one launch over both)
+//   GRADIENTS, one launch for both of
+//     INPUT    dA = dg G + du U            (one sum over both halves)
+//     WEIGHTS  dG = dg^T A,  dU = du^T A
 //
 // A 2-CTA cluster computes a 256-row tile whose MMAs are M = 256, N = 256,
 // K = 16; CTA r holds 128 of A's rows and 128 of B's.  The reduction advances
@@ -25,13 +26,16 @@
 //     their last multiple of 8 columns and the few columns after it are
 //     written from registers: what lies behind a row's end stays as it was.
 // Two accumulators (512 TMEM columns) let each tile's epilogue run beside the
-// next tile's MMAs.  A product of few tiles and a long reduction is split
-// along it (INPUT, WEIGHTS): each part writes fp32 sums to the workspace and
-// a second kernel adds them in order, so results do not depend on timing.
+// next tile's MMAs.  GRADIENTS takes INPUT's tiles first, which are long, and
+// fills the pairs that have fewer of them with more of WEIGHTS' (see tile_of).
+// A product of few tiles and a long reduction is split along it: each part
+// writes fp32 sums to the workspace and a second kernel adds them in order, so
+// results do not depend on timing.
 //
 // Roles as in gemm_pair.cu: warp 0 copies (lane 0 B, lane 1 A), warp 1 issues
 // the MMAs in the even CTA, warps 2-9 are the epilogue, two for each TMEM
 // lane quarter.  Every wait is bounded.
+#include <algorithm>
 #include <cuda_fp16.h>
 
 #include "gated_math.cuh"
@@ -50,9 +54,7 @@ constexpr int MN_BLOCK_BYTES = 64 * 128;  // 64 values x 64 reduction steps
 
 template <int MODE>
 struct Cfg {
-  static constexpr bool kGate = MODE == GATED_FORWARD || MODE == GATED_SLOPES;  // two products a tile
-  static constexpr bool kAMn = MODE == GATED_WEIGHTS;
-  static constexpr bool kBMn = MODE == GATED_INPUT || MODE == GATED_WEIGHTS;
+  static constexpr bool kGate = MODE != GATED_GRADIENTS;  // two products a tile
   static constexpr int kStaging = MODE == GATED_SLOPES ? 2 : 1;  // 4 KiB staging tiles per epilogue warp
   static constexpr int kStages = MODE == GATED_SLOPES ? 5 : 6;
   static constexpr int kEpiBytes = GP_EPI_WARPS * kStaging * 4096;
@@ -106,35 +108,55 @@ __device__ __forceinline__ void stage_row(uint32_t row_addr, int lane, int h, co
 }
 
 // The columns of a row's 32 (from column n) that lie in [tail, cols).
-__device__ __forceinline__ void store_tail(const GatedPairParams& p, int out, int row, int n,
+__device__ __forceinline__ void store_tail(const GatedPairParams& p, const GatedProduct& g, int out, int row, int n,
                                            const uint32_t (&pk)[16]) {
-  if (p.tail >= n + 32 || p.cols <= n || p.tail >= p.cols || row >= p.rows) return;
+  if (g.tail >= n + 32 || g.cols <= n || g.tail >= g.cols || row >= g.rows) return;
   uint16_t* at = p.out[out] + (int64_t)row * p.ld[out] + n;
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
-    if (n + 2 * q >= p.tail && n + 2 * q < p.cols) at[2 * q] = (uint16_t)pk[q];
-    if (n + 2 * q + 1 >= p.tail && n + 2 * q + 1 < p.cols) at[2 * q + 1] = (uint16_t)(pk[q] >> 16);
+    if (n + 2 * q >= g.tail && n + 2 * q < g.cols) at[2 * q] = (uint16_t)pk[q];
+    if (n + 2 * q + 1 >= g.tail && n + 2 * q + 1 < g.cols) at[2 * q + 1] = (uint16_t)(pk[q] >> 16);
   }
 }
 
 }  // namespace
 
-// Tile t of the launch: which output (WEIGHTS) and part of the reduction,
-// and where.
+// The i-th tile of pair `pair` of `pairs`: which product, output (WEIGHTS has
+// two) and part of the reduction, and where.  False past the pair's last.
+// INPUT's tiles go round the pairs.  Where the last round does not reach every
+// pair, the others each take `head` tiles of WEIGHTS meanwhile, about as much
+// work as one of INPUT's, and the rest goes round again: with 256 tiles of 224
+// steps and 896 of 64 on 76 pairs the longest pair has 1536 steps, against
+// 1664 one product after the other (1509 would be even).
 struct TileAt {
-  int out, part, mb, nb, k0, k1;
+  int product, out, part, mb, nb, k0, k1;
 };
 template <int MODE>
-__device__ __forceinline__ TileAt tile_at(int t, const GatedPairParams& p) {
-  TileAt a;
-  const int per = p.tiles_m * p.tiles_n;
+__device__ __forceinline__ bool tile_of(int i, int pair, int pairs, const GatedPairParams& p, TileAt& a) {
+  int t = pair + i * pairs;
+  a.product = 0;
+  if (t >= p.product[0].tiles) {
+    if (MODE != GATED_GRADIENTS) return false;
+    const int over = p.product[0].tiles % pairs;  // pairs with one tile of INPUT more
+    const bool longer = pair < over;
+    const int j = i - (p.product[0].tiles / pairs + (longer ? 1 : 0));
+    const int heads = over > 0 ? p.head : 0, rest = pairs - over;
+    if (!longer && j < heads)
+      t = j * rest + pair - over;
+    else
+      t = heads * rest + (j - (longer ? 0 : heads)) * pairs + pair;
+    if (t >= p.product[1].tiles) return false;
+    a.product = 1;
+  }
+  const GatedProduct& g = p.product[a.product];
+  const int per = g.tiles_m * g.tiles_n;
   const int outer = t / per;
-  a.out = outer / p.parts;
-  a.part = outer - a.out * p.parts;
-  tile_coords(t - outer * per, p.tiles_m, p.tiles_n, p.raster_g, a.mb, a.nb);
-  a.k0 = (int)((int64_t)p.ksteps * a.part / p.parts);
-  a.k1 = (int)((int64_t)p.ksteps * (a.part + 1) / p.parts);
-  return a;
+  a.out = outer / g.parts;
+  a.part = outer - a.out * g.parts;
+  tile_coords(t - outer * per, g.tiles_m, g.tiles_n, g.raster_g, a.mb, a.nb);
+  a.k0 = (int)((int64_t)g.ksteps * a.part / g.parts);
+  a.k1 = (int)((int64_t)g.ksteps * (a.part + 1) / g.parts);
+  return true;
 }
 
 template <int MODE>
@@ -170,14 +192,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     const uint32_t bar = full_leader + (uint32_t)(st * 8);
     uint8_t* dst = s_a + st * OPERAND_BYTES;
     const int row = a.mb * 256 + rank * 128;
-    if constexpr (MODE == GATED_WEIGHTS) {
-      tma_load_2d_pair(dst, &maps.a[a.out], row, ks * 64, bar);
-      tma_load_2d_pair(dst + MN_BLOCK_BYTES, &maps.a[a.out], row + 64, ks * 64, bar);
-    } else if constexpr (MODE == GATED_INPUT) {
+    if constexpr (C::kGate) {
+      tma_load_2d_pair(dst, &maps.a[0], ks * 64, row, bar);
+    } else if (a.product == 0) {
       const int half = ks >= p.ksteps_half ? 1 : 0;
       tma_load_2d_pair(dst, &maps.a[half], (ks - half * p.ksteps_half) * 64, row, bar);
     } else {
-      tma_load_2d_pair(dst, &maps.a[0], ks * 64, row, bar);
+      tma_load_2d_pair(dst, &maps.wa[a.out], row, ks * 64, bar);
+      tma_load_2d_pair(dst + MN_BLOCK_BYTES, &maps.wa[a.out], row + 64, ks * 64, bar);
     }
   };
   auto load_b = [&](int st, const TileAt& a, int ks) {
@@ -186,10 +208,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     if constexpr (C::kGate) {
       tma_load_2d_pair(dst, &maps.b[rank], ks * 64, a.nb * 128, bar);
     } else {
-      const int half = MODE == GATED_INPUT && ks >= p.ksteps_half ? 1 : 0;
+      const int half = a.product == 0 && ks >= p.ksteps_half ? 1 : 0;
+      const CUtensorMap* map = a.product == 0 ? &maps.b[half] : &maps.wb;
       const int col = a.nb * 256 + rank * 128, k = (ks - half * p.ksteps_half) * 64;
-      tma_load_2d_pair(dst, &maps.b[half], col, k, bar);
-      tma_load_2d_pair(dst + MN_BLOCK_BYTES, &maps.b[half], col + 64, k, bar);
+      tma_load_2d_pair(dst, map, col, k, bar);
+      tma_load_2d_pair(dst + MN_BLOCK_BYTES, map, col + 64, k, bar);
     }
   };
 
@@ -219,13 +242,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   // With constant weights the B issuer requests B for the first stages of its
   // first tile before the wait on the previous kernel; A follows after.
   int early = 0;
-  if (MODE == GATED_FORWARD && !bad && p.b_constant && pair < p.num_tiles && threadIdx.x == 0) {
-    const TileAt a = tile_at<MODE>(pair, p);
-    early = min(a.k1 - a.k0, STAGES);
+  TileAt a0;
+  if (MODE == GATED_FORWARD && !bad && p.b_constant && threadIdx.x == 0 && tile_of<MODE>(0, pair, npairs, p, a0)) {
+    early = min(a0.k1 - a0.k0, STAGES);
     for (int i = 0; i < early; ++i) {
       if (p.debug_skip_load == 1 + i) continue;
       if (leader) mbar_arrive_expect_tx(&full[i], 2 * OPERAND_BYTES);
-      load_b(i, a, a.k0 + i);
+      load_b(i, a0, a0.k0 + i);
     }
   }
   pdl_launch_dependents();
@@ -240,8 +263,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       int s = 0;
       uint32_t ph = 0, issued = 0;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
-        const TileAt a = tile_at<MODE>(t, p);
+      TileAt a;
+      for (int i = 0; ok && tile_of<MODE>(i, pair, npairs, p, a); ++i) {
         for (int ks = a.k0; ks < a.k1; ++ks) {
           const bool done = is_b && (int)issued < early;
           if (!done && !wait_bounded(&empty[s], ph ^ 1, abort_flag, p.status, ST_TIMEOUT_PRODUCER, limit)) {
@@ -280,14 +303,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
   } else if (warp == 1) {
     if (leader && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
-      const uint32_t idesc = idesc_dense(p.fp16 ? 0u : 1u, p.fp16 ? 0u : 1u, 256, 256) | (C::kAMn ? kIdescAMn : 0u) |
-                             (C::kBMn ? kIdescBMn : 0u);
+      const uint32_t idesc_k = idesc_dense(p.fp16 ? 0u : 1u, p.fp16 ? 0u : 1u, 256, 256);
       int s = 0;
       uint32_t ph = 0;
-      int local = 0;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs, ++local) {
-        const TileAt a = tile_at<MODE>(t, p);
+      TileAt a;
+      for (int local = 0; ok && tile_of<MODE>(local, pair, npairs, p, a); ++local) {
+        const bool a_mn = !C::kGate && a.product == 1, b_mn = !C::kGate;
+        const uint32_t idesc = idesc_k | (a_mn ? kIdescAMn : 0u) | (b_mn ? kIdescBMn : 0u);
         const int buf = local & 1;
         if (!wait_cluster_bounded(&acce[buf], ((uint32_t)(local >> 1) & 1) ^ 1, abort_flag, p.status, ST_TIMEOUT_MMA,
                                   limit))
@@ -300,12 +323,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(s_a + s * OPERAND_BYTES);
-          const uint32_t b0 = smem_u32(s_b + s * OPERAND_BYTES);
+          const uint32_t sa = smem_u32(s_a + s * OPERAND_BYTES);
+          const uint32_t sb = smem_u32(s_b + s * OPERAND_BYTES);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = C::kAMn ? smem_desc_sw128_mn(a0 + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(a0 + 32 * k);
-            const uint64_t bd = C::kBMn ? smem_desc_sw128_mn(b0 + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(b0 + 32 * k);
+            const uint64_t ad = a_mn ? smem_desc_sw128_mn(sa + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(sa + 32 * k);
+            const uint64_t bd = b_mn ? smem_desc_sw128_mn(sb + 2048 * k, MN_BLOCK_BYTES) : smem_desc_sw128(sb + 32 * k);
             umma_pair<0>(d, ad, bd, idesc, (ks > a.k0 || k > 0) ? 1u : 0u);
           }
           umma_commit_pair(&empty[s], 0x3);
@@ -333,9 +356,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     const bool fp16 = p.fp16 != 0;
     uint64_t* dhb = &dh_bar[warp - 2];
     uint32_t dh_phase = 0;
-    int local = 0;
-    for (int t = pair; t < p.num_tiles; t += npairs, ++local) {
-      const TileAt a = tile_at<MODE>(t, p);
+    TileAt a;
+    for (int local = 0; tile_of<MODE>(local, pair, npairs, p, a); ++local) {
+      const GatedProduct& g = p.product[C::kGate ? 0 : a.product];
       const int buf = local & 1;
       const int row0 = a.mb * 256 + rank * 128 + quad * 32;
       const uint32_t tbase = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * 256);
@@ -344,7 +367,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         // This warp's dH tile, requested while the tile's MMAs still run,
         // into the staging tile that dg will leave from.
         const int n0 = a.nb * 128 + chalf * 64;
-        dh_wanted = row0 < p.rows && n0 < p.cols;
+        dh_wanted = row0 < g.rows && n0 < g.cols;
         if (lane == 0) bulk_wait_group_read<0>();  // the previous stores have read the staging tiles
         if (dh_wanted && lane == 0) {
           mbar_arrive_expect_tx(dhb, 4096);
@@ -362,7 +385,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
       tc_fence_after();
       if constexpr (C::kGate) {
         const int n0 = a.nb * 128 + chalf * 64;
-        const bool inside = row0 < p.rows && n0 < (MODE == GATED_SLOPES ? p.cols : p.tail);
+        const bool inside = row0 < g.rows && n0 < (MODE == GATED_SLOPES ? g.cols : g.tail);
         if constexpr (MODE == GATED_SLOPES) {
           if (dh_wanted) {
             if (!wait_bounded(dhb, dh_phase, abort_flag, p.status, ST_TIMEOUT_EPILOGUE, limit)) break;
@@ -374,9 +397,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t g[32], u[32];
-          tmem_ld_32x32b_x32(tbase + (uint32_t)(chalf * 64 + h * 32), g);
-          tmem_ld_32x32b_x32(tbase + (uint32_t)(128 + chalf * 64 + h * 32), u);
+          uint32_t gr[32], ur[32];
+          tmem_ld_32x32b_x32(tbase + (uint32_t)(chalf * 64 + h * 32), gr);
+          tmem_ld_32x32b_x32(tbase + (uint32_t)(128 + chalf * 64 + h * 32), ur);
           tmem_ld_wait();
           if (h == 1) {  // this warp's last loads of the accumulator: free it
             tc_fence_before();
@@ -390,21 +413,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
               ld_shared_v4(stg_row + (uint32_t)((((h * 4 + q) ^ (lane & 7)) * 16)), d[4 * q], d[4 * q + 1],
                            d[4 * q + 2], d[4 * q + 3]);
             switch (p.act) {
-              case GP_ACT_RELU: slope_row<GP_ACT_RELU>(g, u, d, fp16, dg, du); break;
-              case GP_ACT_SILU: slope_row<GP_ACT_SILU>(g, u, d, fp16, dg, du); break;
-              default: slope_row<GP_ACT_GELU>(g, u, d, fp16, dg, du); break;
+              case GP_ACT_RELU: slope_row<GP_ACT_RELU>(gr, ur, d, fp16, dg, du); break;
+              case GP_ACT_SILU: slope_row<GP_ACT_SILU>(gr, ur, d, fp16, dg, du); break;
+              default: slope_row<GP_ACT_GELU>(gr, ur, d, fp16, dg, du); break;
             }
             stage_row(stg_row, lane, h, dg);  // each lane overwrites what it alone read
             stage_row(stg_row + 4096, lane, h, du);
           } else {
             uint32_t pk[16];
             switch (p.act) {
-              case GP_ACT_RELU: gate_row<GP_ACT_RELU>(g, u, fp16, pk); break;
-              case GP_ACT_SILU: gate_row<GP_ACT_SILU>(g, u, fp16, pk); break;
-              default: gate_row<GP_ACT_GELU>(g, u, fp16, pk); break;
+              case GP_ACT_RELU: gate_row<GP_ACT_RELU>(gr, ur, fp16, pk); break;
+              case GP_ACT_SILU: gate_row<GP_ACT_SILU>(gr, ur, fp16, pk); break;
+              default: gate_row<GP_ACT_GELU>(gr, ur, fp16, pk); break;
             }
             stage_row(stg_row, lane, h, pk);
-            store_tail(p, 0, row0 + lane, n0 + h * 32, pk);
+            store_tail(p, g, 0, row0 + lane, n0 + h * 32, pk);
           }
         }
         fence_proxy_async_smem();
@@ -415,10 +438,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           bulk_commit_group();
         }
       } else {
+        const int out = a.product + a.out;  // dA, dG, dU
 #pragma unroll 1
         for (int c = chalf; c < 4; c += 2) {
           const int n0 = a.nb * 256 + c * 64;
-          const bool inside = row0 < p.rows && n0 < p.tail;
+          const bool inside = row0 < g.rows && n0 < g.tail;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r[32];
@@ -429,7 +453,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acce_leader + (uint32_t)(buf * 8));
             }
-            if (p.parts > 1) {
+            if (g.parts > 1) {
               // fp32 sums of this part: a 32 x 32 tile, 128 bytes a row
               if (lane == 0) bulk_wait_group_read<0>();
               __syncwarp();
@@ -439,8 +463,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                              r[4 * q + 3]);
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0 && row0 < p.rows && n0 + h * 32 < p.cols) {
-                tma_store_3d(&maps.partial, n0 + h * 32, row0, a.out * p.parts + a.part, stg);
+              if (lane == 0 && row0 < g.rows && n0 + h * 32 < g.cols) {
+                tma_store_3d(&maps.partial[a.product], n0 + h * 32, row0, a.out * g.parts + a.part, stg);
                 bulk_commit_group();
               }
             } else {
@@ -455,14 +479,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                 pk[q] = fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
               }
               stage_row(stg_row, lane, h, pk);
-              store_tail(p, a.out, row0 + lane, n0 + h * 32, pk);
+              store_tail(p, g, out, row0 + lane, n0 + h * 32, pk);
             }
           }
-          if (p.parts == 1) {
+          if (g.parts == 1) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && inside) {
-              tma_store_2d(&maps.c[a.out], n0, row0, stg);
+              tma_store_2d(&maps.c[out], n0, row0, stg);
               bulk_commit_group();
             }
           }
@@ -482,33 +506,30 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
 
 namespace {
 
-// out[r, c] = sum of the parts' fp32 sums, in order, rounded once.  blockIdx.y
-// is the output (WEIGHTS has two).
-__global__ void __launch_bounds__(256) gated_add_parts_kernel(const float4* partial, int parts, int64_t rows,
-                                                              int64_t quads, int64_t cols, uint16_t* out0, int64_t ld0,
-                                                              uint16_t* out1, int64_t ld1, int fp16) {
+// out[r, c] = sum of the parts' fp32 sums, in order, rounded once.
+__global__ void __launch_bounds__(256) gated_add_parts_kernel(const __grid_constant__ GatedPartsList list, int fp16) {
   pdl_launch_dependents();
   pdl_wait();
-  uint16_t* out = blockIdx.y == 0 ? out0 : out1;
-  const int64_t ld = blockIdx.y == 0 ? ld0 : ld1;
-  const int64_t slice = rows * quads;
-  partial += blockIdx.y * parts * slice;
+  const GatedParts& g = list.of[blockIdx.y];
+  const float4* partial = reinterpret_cast<const float4*>(g.partial);
+  const int64_t quads = g.pitch / 4, slice = g.rows * quads;
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < slice; x += step) {
     float4 v = partial[x];
-    for (int s = 1; s < parts; ++s) {
+    for (int s = 1; s < g.parts; ++s) {
       const float4 w = partial[s * slice + x];
       v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
     const int64_t r = x / quads, c = (x - r * quads) * 4;
     const uint32_t lo = fp16 ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
     const uint32_t hi = fp16 ? pack_f16x2(v.z, v.w) : pack_bf16x2(v.z, v.w);
-    uint16_t* at = out + r * ld + c;
-    if (c + 4 <= cols) {  // rows start on 16-byte boundaries, c on a multiple of 4
+    uint16_t* at = g.out + r * g.ld + c;
+    if (c + 4 <= g.cols) {  // rows start on 16-byte boundaries, c on a multiple of 4
       *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi);
     } else {
-      const uint32_t w[2] = {lo, hi};
-      for (int e = 0; e < cols - c; ++e) at[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+      if (c < g.cols) at[0] = (uint16_t)lo;
+      if (c + 1 < g.cols) at[1] = (uint16_t)(lo >> 16);
+      if (c + 2 < g.cols) at[2] = (uint16_t)hi;
     }
   }
 }
@@ -520,8 +541,9 @@ int launch_mode(const GatedMaps& maps, GatedPairParams p, int num_sms, cudaStrea
   static std::atomic<bool> attr_set[64];
   if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
   const int pairs = num_sms / 2;
+  const int tiles = p.product[0].tiles + p.product[1].tiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (p.num_tiles < pairs ? p.num_tiles : pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(GP_THREADS);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -544,20 +566,16 @@ int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p,
   switch (mode) {
     case GATED_FORWARD: return launch_mode<GATED_FORWARD>(maps, p, num_sms, stream);
     case GATED_SLOPES: return launch_mode<GATED_SLOPES>(maps, p, num_sms, stream);
-    case GATED_INPUT: return launch_mode<GATED_INPUT>(maps, p, num_sms, stream);
-    default: return launch_mode<GATED_WEIGHTS>(maps, p, num_sms, stream);
+    default: return launch_mode<GATED_GRADIENTS>(maps, p, num_sms, stream);
   }
 }
 
-int gated_add_parts_launch(const float* partial, int parts, int outputs, int64_t rows, int64_t cols, int64_t pitch,
-                           void* out0, int64_t ld0, void* out1, int64_t ld1, bool fp16, int num_sms,
-                           cudaStream_t stream) {
-  const int64_t quads = pitch / 4;
-  int64_t blocks = (rows * quads + 255) / 256;
-  const int64_t most = (int64_t)num_sms * 8;
-  if (blocks > most) blocks = most;
+int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int num_sms, cudaStream_t stream) {
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) most = std::max(most, list.of[i].rows * list.of[i].pitch / 4);
+  const int64_t blocks = std::min<int64_t>((most + 255) / 256, (int64_t)num_sms * 8);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)outputs);
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)count);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -565,10 +583,7 @@ int gated_add_parts_launch(const float* partial, int parts, int outputs, int64_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gated_add_parts_kernel, reinterpret_cast<const float4*>(partial), parts, rows, quads,
-                         cols, static_cast<uint16_t*>(out0), ld0, static_cast<uint16_t*>(out1), ld1,
-                         fp16 ? 1 : 0) != cudaSuccess)
-    return GP_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, gated_add_parts_kernel, list, fp16 ? 1 : 0) != cudaSuccess) return GP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
 }
 

@@ -4,32 +4,40 @@
 
 namespace gp {
 
-enum GatedMode : int { GATED_FORWARD = 0, GATED_SLOPES = 1, GATED_INPUT = 2, GATED_WEIGHTS = 3 };
+enum GatedMode : int { GATED_FORWARD = 0, GATED_SLOPES = 1, GATED_GRADIENTS = 2 };
 
 // Tensor maps of one launch; 128-byte swizzle throughout.  K-major operands
 // have boxes of 64 x 128 rows, MN-major ones 64 x 64, 16-bit outputs (and dH)
 // 64 x 32, fp32 parts 32 x 32 x 1.
 struct GatedMaps {
-  CUtensorMap a[2];     // INPUT: dg, du; WEIGHTS: dg, du (by output); else the activation
-  CUtensorMap b[2];     // gate, up; WEIGHTS: the activation
-  CUtensorMap c[2];     // the outputs
-  CUtensorMap dh;       // SLOPES
-  CUtensorMap partial;  // INPUT, WEIGHTS with parts > 1: [outputs * parts][rows][pitch] fp32
+  CUtensorMap a[2];        // the activation; GRADIENTS: dg, du for INPUT
+  CUtensorMap b[2];        // gate, up (GRADIENTS: MN-major, for INPUT)
+  CUtensorMap wa[2], wb;   // WEIGHTS: dg, du and the activation, MN-major
+  CUtensorMap c[3];        // the outputs; GRADIENTS: dA, dG, dU
+  CUtensorMap dh;          // SLOPES
+  CUtensorMap partial[2];  // GRADIENTS: INPUT's and WEIGHTS' parts, [outputs * parts][rows][pitch] fp32
+};
+
+// One product of a launch: FORWARD, SLOPES and INPUT are product 0, WEIGHTS,
+// with its two outputs, is product 1.
+struct GatedProduct {
+  int rows, cols;        // of one output
+  int tail;              // columns past the last multiple of 8 start here (cols: there are none)
+  int tiles_m, tiles_n;  // 256 rows x 128 (FORWARD, SLOPES) or 256 columns
+  int tiles;             // outputs * parts * tiles_m * tiles_n; 0: not wanted
+  int ksteps;            // reduction steps of 64
+  int parts;             // parts of the reduction, each a tile of its own
+  int raster_g;
 };
 
 struct GatedPairParams {
   uint32_t* status;
   uint64_t wait_limit_ns;
-  int rows, cols;        // of one output
-  uint16_t* out[2];      // the outputs again, for the columns past the last multiple of 8:
-  int64_t ld[2];         // a TMA store writes whole 16-byte units
-  int tail;              // first of those columns, or cols where there are none
-  int tiles_m, tiles_n;  // 256 rows x 128 (FORWARD, SLOPES) or 256 columns
-  int num_tiles;         // outputs * parts * tiles_m * tiles_n
-  int ksteps;            // reduction steps of 64
+  GatedProduct product[2];
   int ksteps_half;       // INPUT: the steps of dg G, before those of du U
-  int parts;             // parts of the reduction, each a tile of its own
-  int raster_g;
+  int head;              // GRADIENTS: see tile_of
+  uint16_t* out[3];      // the outputs again, for the columns past the last multiple of 8:
+  int64_t ld[3];         // a TMA store writes whole 16-byte units
   int act;
   int fp16;
   int b_constant;
@@ -37,10 +45,20 @@ struct GatedPairParams {
 };
 
 int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p, int num_sms, cudaStream_t stream);
-// out = the sum of `parts` fp32 parts, for one or two outputs.
-int gated_add_parts_launch(const float* partial, int parts, int outputs, int64_t rows, int64_t cols, int64_t pitch,
-                           void* out0, int64_t ld0, void* out1, int64_t ld1, bool fp16, int num_sms,
-                           cudaStream_t stream);
+
+// out = the sum of `parts` fp32 parts, in order, for up to three outputs.
+struct GatedParts {
+  const float* partial;  // [parts][rows][pitch]
+  int parts;
+  int64_t rows, cols, pitch;
+  uint16_t* out;
+  int64_t ld;
+};
+struct GatedPartsList {
+  GatedParts of[3];
+};
+int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int num_sms, cudaStream_t stream);
+
 // FORWARD and SLOPES for few tokens or little work (gated_stream.cu): whether
 // it takes them, and the launch, into out0 (and out1 for SLOPES) of pitch ld.
 bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms);
