@@ -50,7 +50,7 @@ bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms) {
   // with the rows of A beside them, and is higher where it has an SM alone.
   const int64_t chunks = (M + 31) / 32, units = (N + 15) / 16 * chunks;
   const int rows = M <= 8 ? 0 : M <= 16 ? 1 : 2;
-  constexpr double kAlone[3] = {73.0, 59.0, 36.0}, kShared[3] = {19.4, 17.0, 16.0};  // KB / us
+  constexpr double kAlone[3] = {73.0, 59.0, 36.0}, kShared[3] = {20.0, 19.0, 16.0};  // KB / us
   const double kb = 0.064 * (double)K, share = (double)units / (2.0 * num_sms);
   const double turns = share <= 1.0 ? 1.0 : chunks == 1 ? share : std::ceil(share);
   const double stream_us = 3.0 + (units <= num_sms ? kb / kAlone[rows] : turns * kb / kShared[rows]);

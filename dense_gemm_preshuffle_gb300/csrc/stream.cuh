@@ -15,9 +15,9 @@
 //     for both: lane t of a row's four takes 8 consecutive values, which are
 //     the values 2t, 2t+1, 2t+8, 2t+9 of two MMAs.  The sum does not change.
 //   - The warps of a block take a row tile's steps in turn; their sums meet in
-//     shared memory in a fixed order.  Each block has a run of row tiles, one
-//     more or less than any other, and the loads of the next tiles are in
-//     flight while some are summed.
+//     shared memory in a fixed order.  A unit of work is R row tiles with 8 NT
+//     rows of A.  Each block has a run of units, one more or less than any
+//     other, and the loads of the next are in flight while one is summed.
 //   - A is read through L1, which keeps it from tile to tile.
 // mma.sync, not tcgen05: at M <= 32 the arithmetic is a few percent of
 // either's rate, and register fragments spare the weights two trips through
@@ -44,7 +44,8 @@ struct StreamParams {
   int M, N, K;
   int steps;                 // steps of a row tile
   int row_tiles;             // ceil(N / 16)
-  int units;                 // row_tiles * chunks of 8 * NT rows of A
+  int groups;                // of R row tiles
+  int units;                 // groups * chunks of 8 * NT rows of A
   int keep_sums;             // 4 bits: room for A's sums in shared memory
   const uint16_t* dH;        // slopes: [M, N]; C is then dg and C2 du
   int64_t lddh;
@@ -100,6 +101,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a . b
+template <bool FP16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  if constexpr (FP16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Eight values of a row of A from k on, as four pairs; zeros from K on.
@@ -168,7 +183,7 @@ struct Rows16 {
 #pragma unroll
           for (int h = 0; h < 2; ++h) at[a][r][h] += WARPS * kStepK * 2;
     }
-    __device__ __forceinline__ void fetch(const StreamParams& p, int tiles, uint32_t dst, int lane) const {
+    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
       // A row's end: the bytes past it are zeros, and never read.
 #pragma unroll
       for (int i = 0; i < HALVES; ++i) {
@@ -176,40 +191,45 @@ struct Rows16 {
 #pragma unroll
         for (int a = 0; a < MATS; ++a)
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= tiles) break;
+          for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               cp_async16(dst + (uint32_t)((a * R + r) * kBytes + ((i * 2 + h) * 32 + lane) * 16),
                          bytes > 0 ? at[a][r][h] + 64 * i : p.W[a], bytes);
-          }
       }
     }
   };
 
-  // The first N row tiles of each matrix.
-  template <int N, int NT>
-  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
+  template <int NT>
+  struct Operand {
+    uint4 x[HALVES][NT];
+    __device__ __forceinline__ void load(const StreamParams& p, const uint16_t* const (&row)[NT], int step, int lane) {
+      const int k0 = step * kStepK + (lane & 3) * 8;
+      if (step * kStepK + kStepK <= p.K) {
+#pragma unroll
+        for (int i = 0; i < HALVES; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < HALVES; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[i][t] = load_a8(row[t], k0 + 32 * i, p.K);
+      }
+    }
+  };
+  template <int NT>
+  static constexpr bool kAhead = NT == 1;  // M = 8, 8192 x 4096: 21.9 us against 22.7; with 16 rows the same
+
+  template <int NT>
+  static __device__ __forceinline__ void multiply(const StreamParams& p, const Operand<NT>& operand, int step,
                                                   uint32_t src, int lane, float*, bool,
                                                   float (&sum)[MATS * R][NT][4]) {
-    uint4 x[HALVES][NT];
-    const int k0 = step * kStepK + (lane & 3) * 8;
-    if (step * kStepK + kStepK <= p.K) {
-#pragma unroll
-      for (int i = 0; i < HALVES; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
-    } else {
-#pragma unroll
-      for (int i = 0; i < HALVES; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[i][t] = load_a8(row[t], k0 + 32 * i, p.K);
-    }
+    const uint4(&x)[HALVES][NT] = operand.x;
 #pragma unroll
     for (int i = 0; i < HALVES; ++i)
 #pragma unroll
       for (int r = 0; r < MATS * R; ++r) {
-        if (r % R >= N) continue;
         const uint32_t at = src + (uint32_t)(r * kBytes + (i * 64 + lane) * 16);
         const uint4 w0 = lds128(at), w1 = lds128(at + 512);
 #pragma unroll
@@ -248,13 +268,12 @@ struct Packed4 {
       at = ((int64_t)tile * p.steps + step) * p.block_bytes + lane * 16;
     }
     __device__ __forceinline__ void advance(const StreamParams& p) { at += WARPS * p.block_bytes; }
-    __device__ __forceinline__ void fetch(const StreamParams& p, int tiles, uint32_t dst, int lane) const {
+    __device__ __forceinline__ void fetch(const StreamParams& p, uint32_t dst, int lane) const {
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
         const uint8_t* src = p.W[a] + at;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          if (r >= tiles) break;
           const uint32_t to = dst + (uint32_t)((a * R + r) * kBytes + lane * 16);
           cp_async16(to, src, 16);
           cp_async16(to + 512, src + 512, 16);
@@ -278,29 +297,37 @@ struct Packed4 {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
 
-  // The first N row tiles of each matrix.
-  template <int N, int NT>
-  static __device__ __forceinline__ void multiply(const StreamParams& p, const uint16_t* const (&row)[NT], int step,
+  template <int NT>
+  struct Operand {
+    uint4 x[4][NT];
+    __device__ __forceinline__ void load(const StreamParams& p, const uint16_t* const (&row)[NT], int step, int lane) {
+      const int k0 = step * 128 + (lane & 3) * 8;
+      if (step * 128 + 128 <= p.K) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
+      } else {  // K % 32 == 0: eight values are all inside or all outside
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            x[i][t] = step * 128 + 32 * i < p.K ? __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i))
+                                                : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  template <int NT>
+  static constexpr bool kAhead = false;  // no faster, and its registers are wanted
+
+  template <int NT>
+  static __device__ __forceinline__ void multiply(const StreamParams& p, const Operand<NT>& operand, int step,
                                                   uint32_t src, int lane, float* kept, bool have,
                                                   float (&sum)[kTiles][NT][4]) {
+    const uint4(&x)[4][NT] = operand.x;
     constexpr uint32_t one = FP16 ? 0x3C003C00u : 0x3F803F80u;
     uint32_t magic;
     asm("mov.b32 %0, %1;" : "=r"(magic) : "n"(FP16 ? 0u : 0x43004300u));
-    uint4 x[4][NT];
-    const int k0 = step * 128 + (lane & 3) * 8;
-    if (step * 128 + 128 <= p.K) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[i][t] = __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i));
-    } else {  // K % 32 == 0: eight values are all inside or all outside
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          x[i][t] = step * 128 + 32 * i < p.K ? __ldg(reinterpret_cast<const uint4*>(row[t] + k0 + 32 * i))
-                                              : make_uint4(0u, 0u, 0u, 0u);
-    }
     // the sums of A by group: every row of the product with ones is the same
     float2 sa[kGroups][NT];
     if (have) {
@@ -314,10 +341,13 @@ struct Packed4 {
       for (int j = 0; j < kGroups; ++j)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float d[4];
 #pragma unroll
           for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
-            mma16816<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
+            if (i == j * (GROUP / 32))
+              mma16816_first<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
+            else
+              mma16816<FP16>(d, one, one, one, one, x[i][t].x, x[i][t].y);
             mma16816<FP16>(d, one, one, one, one, x[i][t].z, x[i][t].w);
           }
           sa[j][t] = make_float2(d[0], d[1]);
@@ -326,7 +356,6 @@ struct Packed4 {
     }
 #pragma unroll
     for (int r = 0; r < kTiles; ++r) {
-      if (r % R >= N) continue;
       const uint4 q0 = lds128(src + (uint32_t)(r * kBytes + lane * 16));
       const uint4 q1 = lds128(src + (uint32_t)(r * kBytes + 512 + lane * 16));
       const uint32_t lo[4] = {q0.x, q0.y, q0.z, q0.w}, hi[4] = {q1.x, q1.y, q1.z, q1.w};
@@ -344,10 +373,6 @@ struct Packed4 {
       for (int j = 0; j < kGroups; ++j) {
         float acc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
-#pragma unroll
         for (int i = j * (GROUP / 32); i < (j + 1) * (GROUP / 32); ++i) {
           const uint32_t w0 = lo[i], w1 = hi[i];
           const uint32_t a0 = pair(w0, magic), a1 = pair(w1, magic);
@@ -356,18 +381,21 @@ struct Packed4 {
           const uint32_t b2 = pair(w0 >> 12, magic), b3 = pair(w1 >> 12, magic);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma16816<FP16>(acc[t], a0, a1, a2, a3, x[i][t].x, x[i][t].y);
+            if (i == j * (GROUP / 32))
+              mma16816_first<FP16>(acc[t], a0, a1, a2, a3, x[i][t].x, x[i][t].y);
+            else
+              mma16816<FP16>(acc[t], a0, a1, a2, a3, x[i][t].x, x[i][t].y);
             mma16816<FP16>(acc[t], b0, b1, b2, b3, x[i][t].z, x[i][t].w);
           }
         }
         const float2 s = scales_of(sw[j], p.scale_fp16);
-        float z0 = 8.0f, z1 = 8.0f;
+        // 128 + z as a float: z is the top of 128's fraction
+        float z0 = 136.0f, z1 = 136.0f;
         if (p.has_zeros) {
-          const uint32_t z = zw[j / 2] >> (16 * (j & 1));
-          z0 = (float)(z & 0xFFu);
-          z1 = (float)((z >> 8) & 0xFFu);
+          z0 = __uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4255 : 0x4055));
+          z1 = __uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4355 : 0x4155));
         }
-        if (!FP16) z0 += 128.0f, z1 += 128.0f;
+        if (FP16) z0 -= 128.0f, z1 -= 128.0f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -383,61 +411,48 @@ struct Packed4 {
 
 // ---------------------------------------------------------------- kernel
 
-template <class P, int TILES, int NT, int STAGES, int WARPS>
+template <class P, int TILES, int NT, int STAGES, int WARPS, int BLOCKS>
 struct StreamCfg {
   static constexpr int kRowPitch = TILES * 16 + 4;  // +4: a warp's fragment stores hit distinct banks
   static constexpr int kStepBytes = TILES * P::kBytes;
   static constexpr int kRing = WARPS * STAGES * kStepBytes;
-  static constexpr int kSmem = kRing + WARPS * 8 * NT * kRowPitch * 4;
+  static constexpr int kRed = WARPS * 8 * NT * kRowPitch;  // floats
+  static constexpr int kRoom = (BLOCKS == 1 ? 227 : 113) * 1024;
+  // Two buffers for the warps' sums, where they fit, save a barrier.
+  static constexpr int kReds = kRing + 2 * kRed * 4 <= kRoom ? 2 : 1;
+  static constexpr int kSmem = kRing + kReds * kRed * 4;
+  static_assert(kSmem <= kRoom, "shared memory budget");
 };
 
-// P: the weights' policy.  MATS matrices, R (1 or 2) row tiles of each a step, 8 * NT
+// P: the weights' policy.  MATS matrices, R row tiles of each a step, 8 * NT
 // rows of A, STAGES steps of the ring, WARPS a block, BLOCKS blocks an SM.
 // SLOPES: dg and du of the gated product in place of it.
 template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES>
 __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid_constant__ StreamParams p) {
-  static_assert(R == 1 || R == 2, "a short step has one tile of each matrix");
   constexpr int TILES = MATS * R;
-  using C = StreamCfg<P, TILES, NT, STAGES, WARPS>;
+  using C = StreamCfg<P, TILES, NT, STAGES, WARPS, BLOCKS>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem + C::kRing);
   [[maybe_unused]] float* sums = reinterpret_cast<float*>(smem + C::kSmem);  // A's, by step, group and row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * C::kStepBytes);
-  // This block's run of (chunk of A's rows, row tile) units, one more or less
-  // than any other's; a step takes up to R row tiles of one chunk.
+  // This block's run of units, one more or less than any other's.
   const int first = (int)((int64_t)p.units * blockIdx.x / gridDim.x);
   const int end = (int)((int64_t)p.units * (blockIdx.x + 1) / gridDim.x);
-  struct Place {
-    int chunk, tile, tiles;
-  };
-  auto place_of = [&](int unit) {
-    Place a;
-    a.chunk = unit / p.row_tiles;
-    a.tile = unit - a.chunk * p.row_tiles;
-    a.tiles = min(R, min(end - unit, p.row_tiles - a.tile));
-    return a;
-  };
-
   // The load cursor runs STAGES - 1 steps ahead of the compute cursor, across units.
   int l_unit = warp < p.steps ? first : end;  // else nothing for this warp
   int l_step = warp, l_slot = 0;
-  Place l_place = place_of(first);
   typename P::Cursor cursor;
-  if (l_unit < end) cursor.start(p, l_place.tile, warp, lane);
+  if (l_unit < end) cursor.start(p, l_unit % p.groups * R, warp, lane);
   auto fetch_next = [&]() {
     if (l_unit < end) {
-      cursor.fetch(p, l_place.tiles, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
+      cursor.fetch(p, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
       l_step += WARPS;
       if (l_step < p.steps) {
         cursor.advance(p);
       } else {
         l_step = warp;
-        l_unit += l_place.tiles;
-        if (l_unit < end) {
-          l_place = place_of(l_unit);
-          cursor.start(p, l_place.tile, warp, lane);
-        }
+        if (++l_unit < end) cursor.start(p, l_unit % p.groups * R, warp, lane);
       }
       if (++l_slot == STAGES) l_slot = 0;
     }
@@ -455,12 +470,14 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     pdl_wait();
   }
 
-  int slot = 0, of_chunk = -1;
-  for (int unit = first; unit < end;) {
-    const Place at = place_of(unit);
-    const int m0 = at.chunk * (8 * NT);
-    const bool have = P::kSums > 0 && p.keep_sums && of_chunk == at.chunk;
-    of_chunk = at.chunk;
+  int slot = 0, of_chunk = -1, red_at = 0;
+  [[maybe_unused]] typename P::template Operand<NT> ahead;  // of the warp's next step, where registers allow
+  for (int unit = first; unit < end; ++unit) {
+    const int chunk = unit / p.groups, tile = (unit - chunk * p.groups) * R;
+    const int m0 = chunk * (8 * NT);
+    const bool same_rows = of_chunk == chunk;
+    const bool have = P::kSums > 0 && p.keep_sums && same_rows;
+    of_chunk = chunk;
     const uint16_t* row[NT];  // rows past M repeat the last: their sums are not stored
 #pragma unroll
     for (int t = 0; t < NT; ++t) row[t] = p.A + (int64_t)min(m0 + t * 8 + (lane >> 2), p.M - 1) * p.lda;
@@ -472,20 +489,25 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[r][t][e] = 0.0f;
 
+    if (P::template kAhead<NT> && !same_rows && warp < p.steps) ahead.load(p, row, warp, lane);
     for (int step = warp; step < p.steps; step += WARPS) {
+      typename P::template Operand<NT> operand;
+      if constexpr (P::template kAhead<NT>) {
+        operand = ahead;
+        ahead.load(p, row, step + WARPS < p.steps ? step + WARPS : warp, lane);  // on to the next row tiles
+      } else {
+        operand.load(p, row, step, lane);
+      }
       cp_async_wait<STAGES - 2>();
       if (P::kShared) __syncwarp();  // every lane's bytes are there, and the slot fetched into below has been read
       float* kept = P::kSums > 0 && p.keep_sums ? sums + step * (P::kSums * 8 * NT) : nullptr;
-      if (at.tiles == R)
-        P::template multiply<R, NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
-      else
-        P::template multiply<1, NT>(p, row, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
+      P::template multiply<NT>(p, operand, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
       fetch_next();  // into the slot that the step before this one read
       if (++slot == STAGES) slot = 0;
     }
 
     // The warps' sums, [warp][row of A][weight row], added in warp order.
-    float* mine = red + warp * 8 * NT * C::kRowPitch;
+    float* mine = red + red_at + warp * 8 * NT * C::kRowPitch;
 #pragma unroll
     for (int r = 0; r < TILES; ++r)
 #pragma unroll
@@ -498,13 +520,13 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     const int used = min(WARPS, p.steps);  // warps past that hold zeros
     for (int x = threadIdx.x; x < live * R * 16; x += 32 * WARPS) {
       const int m = x / (R * 16), n = x % (R * 16);
-      const int64_t col = (int64_t)at.tile * 16 + n;
-      if (n >= at.tiles * 16 || col >= p.N) continue;
+      const int64_t col = (int64_t)tile * 16 + n;
+      if (col >= p.N) continue;
       float v[MATS];
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
         v[a] = 0.0f;
-        for (int w = 0; w < used; ++w) v[a] += red[(w * 8 * NT + m) * C::kRowPitch + a * R * 16 + n];
+        for (int w = 0; w < used; ++w) v[a] += red[red_at + (w * 8 * NT + m) * C::kRowPitch + a * R * 16 + n];
       }
       const int64_t to = (int64_t)(m0 + m) * p.ldc + col;
       if constexpr (SLOPES) {
@@ -517,27 +539,30 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
         p.C[to] = round16<P::FP16>(MATS == 2 ? act_of(v[0], p.act).value * v[MATS - 1] : v[0]);
       }
     }
-    __syncthreads();  // before the next unit's sums replace these
-    unit += at.tiles;
+    // before the next sums replace these: with two buffers, the next barrier
+    // lies between
+    if (C::kReds == 1)
+      __syncthreads();
+    else
+      red_at ^= C::kRed;
   }
   cp_async_wait<0>();
 }
 
 template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES = false>
 int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
-  using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS>;
+  using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS, BLOCKS>;
   auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS, SLOPES>;
   static std::atomic<bool> attr_set[64];
-  constexpr int kRoom = (BLOCKS == 1 ? 227 : 113) * 1024;
-  static_assert(C::kSmem <= kRoom, "shared memory budget");
-  if (const int rc = smem_attr_once(attr_set, kern, P::kSums > 0 ? kRoom : C::kSmem); rc != GP_OK) return rc;
-  const int64_t units = p.row_tiles * (((int64_t)p.M + 8 * NT - 1) / (8 * NT));
+  if (const int rc = smem_attr_once(attr_set, kern, P::kSums > 0 ? C::kRoom : C::kSmem); rc != GP_OK) return rc;
+  p.groups = (p.row_tiles + R - 1) / R;
+  const int64_t units = p.groups * (((int64_t)p.M + 8 * NT - 1) / (8 * NT));
   if (units > 0x40000000) return GP_ERR_SHAPE;  // more outputs than the memory holds
   p.units = (int)units;
   // A's sums are kept where a block has several units and they fit.
   const int slots = BLOCKS * num_sms;
   const int64_t sums = (int64_t)p.steps * P::kSums * 8 * NT * 4;
-  p.keep_sums = P::kSums > 0 && units > slots && C::kSmem + sums <= kRoom ? 1 : 0;
+  p.keep_sums = P::kSums > 0 && units > slots && C::kSmem + sums <= C::kRoom ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.units < slots ? p.units : slots));
   cfg.blockDim = dim3(32 * WARPS);

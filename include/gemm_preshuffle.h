@@ -403,7 +403,7 @@ int gemm_unpack_w4g(const void* packed, int64_t N, int64_t K, int group, int has
  *             preceding kernel on `stream` has finished; GP_RUN_INDEPENDENT is
  *             taken as that.
  * Codes enter the products exactly; sums are fp32; one rounding at the end.
- * The weights are read once per 32 rows of A, so this is for small M; any
+ * The weights are read once per 16 rows of A, so this is for small M; any
  * M < 2^31 is accepted.  Finite A is expected (|A| < 2^100 for bf16): rows
  * with infinities or NaN give infinities or NaN.  Results are the same bits
  * for the same inputs.  One kernel on `stream`; nothing is allocated.
