@@ -332,11 +332,12 @@ def _matrix(name: str, t, shape, dtype) -> int:
 
 
 def _new_rows(like, rows: int, cols: int):
-    """An empty [rows, cols] matrix of like's type whose rows start on 16-byte boundaries."""
+    """An empty [rows, cols] matrix of like's type whose rows start on
+    16-byte boundaries: a pitch of cols rounded up to 8."""
     import torch
     if cols % 8 == 0:
         return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
-    return torch.empty((rows, (cols + 7) // 8 * 8), dtype=like.dtype, device=like.device)[:, :cols]
+    return torch.empty_strided((rows, cols), ((cols + 7) // 8 * 8, 1), dtype=like.dtype, device=like.device)
 
 
 def _stream_for(t, stream) -> Optional[int]:
@@ -362,11 +363,12 @@ def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_co
     N = W_gate.shape[0]
     lda, ldg, ldu = _matrix("A", A, (M, K), t), _matrix("W_gate", W_gate, (N, K), t), _matrix("W_up", W_up, (N, K), t)
     if out is None:
-        out = _new_rows(A, M, N)
+        out, ldh = _new_rows(A, M, N), (N + 7) // 8 * 8
+    else:
+        ldh = _matrix("out", out, (M, N), t)
     _check((_lib or load_library()).gemm_gated_run(
-        A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dt, M, N, K, _act(act), out.data_ptr(),
-        _matrix("out", out, (M, N), t), GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT,
-        _stream_for(A, stream)), "gemm_gated_run")
+        A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dt, M, N, K, _act(act), out.data_ptr(), ldh,
+        GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, _stream_for(A, stream)), "gemm_gated_run")
     return out
 
 
