@@ -304,6 +304,7 @@ def matmul(A, B_packed, dtype, N: int, K: int, scale_a=None, scale_b=None, out=N
 
 
 _float16_types = None
+_raw_stream = None
 
 
 def _float16_type(t) -> int:
@@ -318,7 +319,9 @@ def _float16_type(t) -> int:
 
 
 def _matrix(name: str, t, shape, dtype) -> int:
-    """Checks a device matrix with contiguous rows and returns its row pitch."""
+    """Checks a device matrix with contiguous rows and returns its row pitch.
+    (Every attribute of a tensor that is looked at costs a small call about
+    1% of its host time.)"""
     if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name}: a {dtype} CUDA tensor of shape {tuple(shape)} is wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -335,8 +338,6 @@ def _new_rows(like, rows: int, cols: int):
     """An empty [rows, cols] matrix of like's type whose rows start on
     16-byte boundaries: a pitch of cols rounded up to 8."""
     import torch
-    if cols % 8 == 0:
-        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
     return torch.empty_strided((rows, cols), ((cols + 7) // 8 * 8, 1), dtype=like.dtype, device=like.device)
 
 
@@ -344,9 +345,12 @@ def _stream_for(t, stream) -> Optional[int]:
     """The launch stream: `stream`, or torch's current one on t's device.
     (The raw handle: building torch's Stream object takes 3 us of host time,
     as long as a small product.)"""
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        if _raw_stream is None:
+            import torch
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(t.get_device())
     return _stream(stream)
 
 
@@ -366,9 +370,11 @@ def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_co
         out, ldh = _new_rows(A, M, N), (N + 7) // 8 * 8
     else:
         ldh = _matrix("out", out, (M, N), t)
-    _check((_lib or load_library()).gemm_gated_run(
+    code = (_lib or load_library()).gemm_gated_run(
         A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dt, M, N, K, _act(act), out.data_ptr(), ldh,
-        GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, _stream_for(A, stream)), "gemm_gated_run")
+        GP_RUN_B_CONSTANT if b_constant else GP_RUN_DEFAULT, _stream_for(A, stream))
+    if code != GP_OK:
+        raise GemmError(code, "gemm_gated_run")
     return out
 
 

@@ -16,26 +16,52 @@ constexpr int kPairs = 76;
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t cdiv(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// Parts that the reductions of the gradients' two products are split into.
-// With tiles enough for every pair of SMs there is one; else a tile is cut to
-// about the load of a pair if all pairs shared the work evenly (six steps at
-// the least), where that pays for the fp32 parts' way through memory, twice 4
-// bytes at about 5 TB/s, and one more launch.  A step of 64 takes 0.28 us.
+// Parts that the reductions of the gradients' two products are split into:
+// what takes the fewest microseconds by a model of the launch (tile_of in
+// gated_pair.cu is its order), whose rates are those measured where few tiles
+// run: 0.36 us for a step of 64, one step more for a tile's change (and five at
+// the least: its epilogue), 2 us for
+// the launch that adds the parts and 16 TB/s (L2) for their two passes through
+// memory, or 5 where they exceed L2.  5719 x 384 x 384, whole and in the 12
+// parts that it takes: 51.1 and 28.9 us; 256 x 4096 x 4096, 80.2 and 67.1 with
+// 2.  Both products are counted whether or not a call wants both, so that what
+// it wants does not change a gradient's sums.
 struct Parts {
   int input, weights;
 };
+
+int64_t tile_steps(int64_t ksteps, int parts) { return std::max<int64_t>(cdiv(ksteps, parts) + 1, 5); }
+
+int64_t heads_of(int64_t input_steps, int64_t weight_steps) { return (input_steps + weight_steps / 2) / weight_steps; }
+
 Parts parts_of(int64_t M, int64_t N, int64_t K) {
   const int64_t ti = cdiv(M, 256) * cdiv(K, 256), tw = 2 * cdiv(N, 256) * cdiv(K, 256);
   const int64_t ki = 2 * cdiv(N, 64), kw = cdiv(M, 64);
-  const int64_t load = std::max<int64_t>(cdiv(ti * ki + tw * kw, kPairs), 6);
-  auto split = [&](int64_t k) { return (int)std::min<int64_t>(cdiv(k, load), 16); };
-  const Parts p{split(ki), split(kw)};
-  const int64_t whole = std::max({load, ki, kw});
-  const int64_t cut = std::max({load, cdiv(ki, p.input), cdiv(kw, p.weights)});
-  const double bytes = 8.0 * (double)K * ((p.input > 1 ? (double)p.input * M : 0.0) +
-                                          (p.weights > 1 ? 2.0 * p.weights * N : 0.0));
-  if (0.28 * (double)(whole - cut) <= 3.0 + bytes / 5.0e6) return {1, 1};
-  return p;
+  if (std::max(ki, kw) * 4 * kPairs <= ti * ki + tw * kw) return {1, 1};  // no tile is long beside the whole
+  auto steps = [&](int pi, int pw) {  // of the pair with most
+    const int64_t Ti = ti * pi, Tw = tw * pw, si = tile_steps(ki, pi), sw = tile_steps(kw, pw);
+    if (Ti + Tw <= kPairs) return std::max(si, sw);
+    const int64_t over = Ti % kPairs, rest = kPairs - over, heads = over > 0 ? heads_of(si, sw) : 0;
+    const int64_t taken = std::min(heads, cdiv(Tw, rest)), left = std::max<int64_t>(Tw - heads * rest, 0);
+    const int64_t rounds = left / kPairs, more = left % kPairs;
+    const int64_t longer = over > 0 ? (Ti / kPairs + 1) * si + (rounds + (more > 0)) * sw : 0;
+    return std::max(longer, Ti / kPairs * si + (taken + rounds + (more > over)) * sw);
+  };
+  Parts best{1, 1};
+  double best_us = 0.0;
+  for (int pi : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    if (pi > 1 && pi * 4 > ki) break;
+    for (int pw : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (pw > 1 && pw * 4 > kw) break;
+      double us = 0.36 * (double)steps(pi, pw);
+      if (pi * pw > 1) {
+        const double bytes = 8.0 * (double)K * ((pi > 1 ? (double)pi * M : 0.0) + (pw > 1 ? 2.0 * pw * N : 0.0));
+        us += 2.0 + bytes / (bytes < 1.0e8 ? 16.0e6 : 5.0e6);
+      }
+      if (pi * pw == 1 || us < best_us) best = {pi, pw}, best_us = us;
+    }
+  }
+  return best;
 }
 
 // dg | du | INPUT's fp32 parts | WEIGHTS' fp32 parts
@@ -198,9 +224,8 @@ int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream
   }
   if (e.rc != GP_OK) return e.rc;
   if (input && weights) {
-    // tiles of WEIGHTS that take as long as one of INPUT's, four steps of each for its ends
-    const int ki = p.product[0].ksteps / p.product[0].parts + 4, kw = p.product[1].ksteps / p.product[1].parts + 4;
-    p.head = (ki + kw / 2) / kw;
+    p.head = (int)heads_of(tile_steps(p.product[0].ksteps, p.product[0].parts),
+                           tile_steps(p.product[1].ksteps, p.product[1].parts));
   }
   if ((rc = gated_pair_launch(GATED_GRADIENTS, maps, p, ctx.num_sms, stream)) != GP_OK || lists == 0) return rc;
   return gated_add_parts_launch(list, lists, a.fp16, ctx.num_sms, stream);

@@ -17,13 +17,19 @@ template <bool FP16, int GROUP, int NT>
 int w4g_launch_nt(const StreamParams& p, bool gated, int num_sms, cudaStream_t stream) {
   // Two tiles of each matrix a step share A's loads and sums; one where no
   // block has two.  A pair of matrices with two tiles each fits the registers
-  // only beside 8 rows of A and few scales.
-  const bool two = (int64_t)p.row_tiles * ((p.M + 8 * NT - 1) / (8 * NT)) > 2 * num_sms;
+  // only beside 8 rows of A and few scales.  With 16 rows, whose loads weigh
+  // more, four tiles of one matrix where that leaves three blocks for every
+  // two SMs (16 x 14528 x 12896: 46.4 -> 38.5 us, 16 x 8192 x 4096, with fewer
+  // blocks than SMs: 9.1 -> 13.3).
+  const int64_t units = (int64_t)p.row_tiles * ((p.M + 8 * NT - 1) / (8 * NT));
+  const bool two = units > 2 * num_sms;
   if (gated) {
     if constexpr (NT == 1 && GROUP >= 64)
       if (two) return w4g_launch_r<FP16, GROUP, 2, 2, NT>(p, num_sms, stream);
     return w4g_launch_r<FP16, GROUP, 2, 1, NT>(p, num_sms, stream);
   }
+  if constexpr (NT == 2 && GROUP == 128)
+    if (units >= 6 * num_sms) return w4g_launch_r<FP16, GROUP, 1, 4, NT>(p, num_sms, stream);
   return two ? w4g_launch_r<FP16, GROUP, 1, 2, NT>(p, num_sms, stream)
              : w4g_launch_r<FP16, GROUP, 1, 1, NT>(p, num_sms, stream);
 }
