@@ -12,8 +12,16 @@ constexpr int64_t kMaxDim = int64_t(1) << 31;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+
+// Whether a matrix of these sizes could not be addressed: 2^50 elements are
+// far past any memory, and the byte counts below stay within 63 bits.
+bool too_large(int64_t M, int64_t N, int64_t K) {
+  const double most = 1125899906842624.0;  // 2^50
+  return (double)M * (double)N > most || (double)M * (double)K > most || (double)N * (double)K > most;
+}
+
 bool bad_dims(int64_t M, int64_t N, int64_t K) {
-  return M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim;
+  return M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || too_large(M, N, K);
 }
 
 // A pitch in 16-bit elements: every row on a 16-byte boundary, and within
@@ -159,7 +167,7 @@ int gemm_run_w4g(const void* A, int64_t lda, int dtype, const void* W_packed, co
   if (rc == GP_OK) rc = check_type(scale_dtype);
   if (rc == GP_OK) rc = check_w4g(N, K, group, has_zeros);
   if (rc != GP_OK) return rc;
-  if (M < 0 || M >= kMaxDim || bad_pitch(lda, K) || ldc < N) return GP_ERR_SHAPE;
+  if (bad_dims(M, N, K) || bad_pitch(lda, K) || ldc < N) return GP_ERR_SHAPE;
   if (M == 0 || N == 0) return GP_OK;
   if (C == nullptr || (K > 0 && (A == nullptr || W_packed == nullptr))) return GP_ERR_INVALID_ARG;
   if (!aligned16(C) || (K > 0 && (!aligned16(A) || !aligned16(W_packed) || !aligned16(U_packed))))

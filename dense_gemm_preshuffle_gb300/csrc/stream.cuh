@@ -292,11 +292,6 @@ struct Packed4 {
     return v;
   }
 
-  static __device__ __forceinline__ float2 scales_of(uint32_t w, int scale_fp16) {
-    if (scale_fp16) return __half22float2(*reinterpret_cast<__half2*>(&w));
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-
   template <int NT>
   struct Operand {
     uint4 x[4][NT];
@@ -354,21 +349,58 @@ struct Packed4 {
           if (kept != nullptr && lane < 4) *reinterpret_cast<float2*>(kept + (j * NT + t) * 8 + 2 * lane) = sa[j][t];
         }
     }
+    // Scales and zero points (as 128 + z: z is the top of 128's fraction) of
+    // rows g and g + 8.  The two kinds of branches on the call's arguments are
+    // taken once for all tiles, or once a tile where that needs registers, so
+    // that the arithmetic below is one run of instructions.
+    constexpr int kEarly = kTiles * kGroups <= 4 ? kTiles : 1;
+    float2 s[kEarly][kGroups], z[kEarly][kGroups];
+    auto load_scales = [&](int first) {
+      uint32_t sw[kEarly][kGroups];
+#pragma unroll
+      for (int r = 0; r < kEarly; ++r)
+        lds_words(src + (uint32_t)((first + r) * kBytes + 1024 + (lane >> 2) * (kGroups * 4)), sw[r]);
+      if (p.has_zeros) {
+#pragma unroll
+        for (int r = 0; r < kEarly; ++r) {
+          uint32_t zw[(kGroups + 1) / 2];  // two bytes a group
+          const uint32_t az = src + (uint32_t)((first + r) * kBytes + 1024 + kGroups * 32 + (lane >> 2) * (kGroups * 2));
+          if constexpr (kGroups == 1)
+            zw[0] = lds_u16(az);
+          else
+            lds_words(az, zw);
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j)
+            z[r][j] = make_float2(__uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4255 : 0x4055)),
+                                  __uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4355 : 0x4155)));
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kEarly; ++r)
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) z[r][j] = make_float2(136.0f, 136.0f);
+      }
+      if (p.scale_fp16) {
+#pragma unroll
+        for (int r = 0; r < kEarly; ++r)
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) s[r][j] = __half22float2(*reinterpret_cast<__half2*>(&sw[r][j]));
+      } else {
+#pragma unroll
+        for (int r = 0; r < kEarly; ++r)
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j)
+            s[r][j] = make_float2(__uint_as_float(sw[r][j] << 16), __uint_as_float(sw[r][j] & 0xFFFF0000u));
+      }
+    };
+    if (kEarly == kTiles) load_scales(0);
 #pragma unroll
     for (int r = 0; r < kTiles; ++r) {
+      const int e0 = kEarly == kTiles ? r : 0;
+      if (kEarly != kTiles) load_scales(r);
       const uint4 q0 = lds128(src + (uint32_t)(r * kBytes + lane * 16));
       const uint4 q1 = lds128(src + (uint32_t)(r * kBytes + 512 + lane * 16));
       const uint32_t lo[4] = {q0.x, q0.y, q0.z, q0.w}, hi[4] = {q1.x, q1.y, q1.z, q1.w};
-      uint32_t sw[kGroups], zw[(kGroups + 1) / 2];  // rows g and g + 8: two scales, two zero points a group
-      const uint32_t at = src + (uint32_t)(r * kBytes + 1024 + (lane >> 2) * (kGroups * 4));
-      lds_words(at, sw);
-      if (p.has_zeros) {
-        const uint32_t az = src + (uint32_t)(r * kBytes + 1024 + kGroups * 32 + (lane >> 2) * (kGroups * 2));
-        if constexpr (kGroups == 1)
-          zw[0] = lds_u16(az);
-        else
-          lds_words(az, zw);
-      }
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
         float acc[NT][4];
@@ -388,19 +420,12 @@ struct Packed4 {
             mma16816<FP16>(acc[t], b0, b1, b2, b3, x[i][t].z, x[i][t].w);
           }
         }
-        const float2 s = scales_of(sw[j], p.scale_fp16);
-        // 128 + z as a float: z is the top of 128's fraction
-        float z0 = 136.0f, z1 = 136.0f;
-        if (p.has_zeros) {
-          z0 = __uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4255 : 0x4055));
-          z1 = __uint_as_float(__byte_perm(zw[j / 2], 0x43u, j & 1 ? 0x4355 : 0x4155));
-        }
-        if (FP16) z0 -= 128.0f, z1 -= 128.0f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float zz = e < 2 ? z0 : z1, ss = e < 2 ? s.x : s.y, of_a = e & 1 ? sa[j][t].y : sa[j][t].x;
+            const float zz = (e < 2 ? z[e0][j].x : z[e0][j].y) - (FP16 ? 128.0f : 0.0f);
+            const float ss = e < 2 ? s[e0][j].x : s[e0][j].y, of_a = e & 1 ? sa[j][t].y : sa[j][t].x;
             const float v = FP16 ? fmaf(acc[t][e], 16777216.0f, -zz * of_a) : fmaf(-zz, of_a, acc[t][e]);
             sum[r][t][e] = fmaf(ss, v, sum[r][t][e]);
           }

@@ -306,8 +306,11 @@ typedef enum gp_act {
  * `stream` (K == 0: an async memset); nothing is allocated.
  * Errors: GP_ERR_INVALID_ARG (null pointer, unknown dtype value, act or
  * flag), GP_ERR_UNSUPPORTED (dtype is not a 16-bit float), GP_ERR_SHAPE (a
- * size is negative or >= 2^31, or a pitch is shorter than its row or not a
- * multiple of 8), GP_ERR_ALIGNMENT (a pointer is not 16-byte aligned).
+ * size is negative or >= 2^31, a matrix has more than 2^50 elements, or a
+ * pitch is shorter than its row or not a multiple of 8), GP_ERR_ALIGNMENT (a
+ * pointer is not 16-byte aligned).
+ * Which of two kernels runs, the one on tensor-core tiles or the one that
+ * streams the weights past few tokens, follows from the sizes alone.
  */
 int gemm_gated_run(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu, int dtype,
                    int64_t M, int64_t N, int64_t K, int act, void* H, int64_t ldh, unsigned flags, void* stream);
@@ -325,8 +328,9 @@ int gemm_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t*
  *   dg = dH * u * act'(g)      du = dH * act(g)
  *   dA = dg G + du U           dG = dg^T A           dU = du^T A
  *
- * dg and du are rounded to dtype (they are operands of the tensor cores);
- * everything else is fp32 until each result's one rounding.
+ * dg and du are rounded to dtype (they are operands of the tensor cores; in
+ * fp16, beyond 65504 they are infinite, so a loss is scaled as for any fp16
+ * gradient); everything else is fp32 until each result's one rounding.
  *
  * dH : device, [M, N], pitch lddh.
  * dA : device, [M, K], pitch ldda, or NULL where A needs no gradient.
@@ -425,7 +429,8 @@ const char* gemm_status_string(int status);
  * load of that stage and of every later stage is skipped.
  * The waits for that stage then time out after the wait limit, which
  * defaults to 2 s and is overridden by the environment variable
- * GP_WAIT_LIMIT_MS, read once per process.
+ * GP_WAIT_LIMIT_MS, read once per process.  The tile kernels of the gated
+ * products take the armed index too.
  *
  * When the wait times out, the kernel drains its in-flight copies, frees
  * any tensor memory and exits.  The library's status word is set, and

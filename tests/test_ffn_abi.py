@@ -168,3 +168,13 @@ def test_dequantize_by_hand():
     assert w[0, 0] == 0.0 and w[0, 1] == 0.5          # (1 - 1) / 2, (2 - 1) / 2
     assert w[0, 62] == 0.0 and w[0, 63] == 2.0        # (3 - 3) * 2, (4 - 3) * 2
     assert ffn.w4g_dequantize(codes, scales, None, 32)[0, 63] == -8.0
+
+
+def test_sizes_past_any_memory(lib):
+    big = (1 << 31) - 1
+    out = ctypes.c_size_t(0)
+    assert lib.gemm_gated_backward_workspace_bytes(big, big, 8, ctypes.byref(out)) == 3
+    assert lib.gemm_packed_w4g_bytes(big, big - 31, 128, 0, ctypes.byref(out)) == 3
+    a = {**RUN, "M": big, "N": big, "ldh": 1 << 31}
+    assert lib.gemm_gated_run(*[a[k] for k in RUN], None) == 3
+    assert gp.gemm_gated_backward_workspace_bytes(1 << 20, 1 << 20, 64) >= 4 << 40
