@@ -13,28 +13,30 @@ namespace {
 
 constexpr int kHalves = 2;  // 128 contiguous bytes of a row a step: 64 cost a third of the bandwidth
 
-template <bool FP16, int NT, bool SLOPES, int WARPS, int BLOCKS>
+template <bool FP16, int NT, bool SLOPES, int WARPS, int BLOCKS, int CLUSTER>
+int launch_as(const StreamParams& p, int num_sms, cudaStream_t stream) {
+  constexpr int STAGES = NT == 1 ? 3 : 2;  // what fits beside the warps' sums
+  return launch_stream<Rows16<FP16, kHalves, 2, 1, WARPS * CLUSTER>, 2, 1, NT, STAGES, WARPS, BLOCKS, CLUSTER, SLOPES>(
+      p, num_sms, stream);
+}
+
+template <bool FP16, int NT, bool SLOPES>
 int launch_nt(const StreamParams& p, int num_sms, cudaStream_t stream) {
-  // three stages, or the two that fit beside 32 rows' sums
-  constexpr int kRed = WARPS * 8 * NT * 36 * 4, kStep = WARPS * 2 * kHalves * 1024;
-  constexpr int kFit = ((BLOCKS == 1 ? 227 : 113) * 1024 - kRed) / kStep, STAGES = kFit < 3 ? kFit : 3;
-  return launch_stream<Rows16<FP16, kHalves, 2, 1, WARPS>, 2, 1, NT, STAGES, WARPS, BLOCKS, SLOPES>(p, num_sms,
-                                                                                                   stream);
+  const int64_t units = (int64_t)p.row_tiles * ((p.M + 8 * NT - 1) / (8 * NT));
+  // Few units: a cluster of blocks each, if all run at once and K is long
+  // enough for the cluster's barriers (8 x 500 x 8192: 9.0 -> 5.8 us; at 32 x
+  // 1000 x 1000 5.7, where 16 warps and an SM to each block take 4.0, and the
+  // common form 5.2).
+  if (units * 4 <= 2 * num_sms && p.steps >= 48) return launch_as<FP16, NT, SLOPES, 8, 2, 4>(p, num_sms, stream);
+  if (units <= num_sms) return launch_as<FP16, NT, SLOPES, 16, 1, 1>(p, num_sms, stream);
+  return launch_as<FP16, NT, SLOPES, 8, 2, 1>(p, num_sms, stream);
 }
 
 template <bool FP16, bool SLOPES>
 int launch_type(const StreamParams& p, int num_sms, cudaStream_t stream) {
-  // Few units: a block has an SM to itself, and twice the warps (1 x 1024 x
-  // 8192, 64 units: 9.6 us against 15.3 with 8 warps).
-  const bool few = (int64_t)p.row_tiles * ((p.M + 31) / 32) <= num_sms;
-  if (p.M <= 8)
-    return few ? launch_nt<FP16, 1, SLOPES, 16, 1>(p, num_sms, stream)
-               : launch_nt<FP16, 1, SLOPES, 8, 2>(p, num_sms, stream);
-  if (p.M <= 16)
-    return few ? launch_nt<FP16, 2, SLOPES, 16, 1>(p, num_sms, stream)
-               : launch_nt<FP16, 2, SLOPES, 8, 2>(p, num_sms, stream);
-  return few ? launch_nt<FP16, 4, SLOPES, 16, 1>(p, num_sms, stream)
-             : launch_nt<FP16, 4, SLOPES, 8, 2>(p, num_sms, stream);
+  if (p.M <= 8) return launch_nt<FP16, 1, SLOPES>(p, num_sms, stream);
+  if (p.M <= 16) return launch_nt<FP16, 2, SLOPES>(p, num_sms, stream);
+  return launch_nt<FP16, 4, SLOPES>(p, num_sms, stream);
 }
 
 }  // namespace
@@ -47,13 +49,16 @@ bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms) {
   if (forced >= 0) return forced != 0;
   // Microseconds of each form by its measured rates, and the smaller.
   // Streaming: a unit reads 16 rows of G and of U; the rate of a block falls
-  // with the rows of A beside them, and is higher where it has an SM alone.
+  // with the rows of A beside them, and is higher where it has an SM alone, or
+  // four share the unit.
   const int64_t chunks = (M + 31) / 32, units = (N + 15) / 16 * chunks;
   const int rows = M <= 8 ? 0 : M <= 16 ? 1 : 2;
   constexpr double kAlone[3] = {73.0, 59.0, 36.0}, kShared[3] = {20.0, 19.0, 16.0};  // KB / us
   const double kb = 0.064 * (double)K, share = (double)units / (2.0 * num_sms);
   const double turns = share <= 1.0 ? 1.0 : chunks == 1 ? share : std::ceil(share);
-  const double stream_us = 3.0 + (units <= num_sms ? kb / kAlone[rows] : turns * kb / kShared[rows]);
+  const bool cluster = units * 4 <= 2 * num_sms && K > 47 * 64;
+  const double alone = kAlone[rows] * (cluster ? 1.7 : 1.0);
+  const double stream_us = 3.0 + (units <= num_sms ? kb / alone : turns * kb / kShared[rows]);
   // Tiles: 0.285 us for 64 values of K on every pair's tile, or the weights' reading.
   const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128), pairs = num_sms / 2;
   const double waves = (double)((tiles + pairs - 1) / pairs);

@@ -436,7 +436,7 @@ struct Packed4 {
 
 // ---------------------------------------------------------------- kernel
 
-template <class P, int TILES, int NT, int STAGES, int WARPS, int BLOCKS>
+template <class P, int TILES, int NT, int STAGES, int WARPS, int BLOCKS, int CLUSTER>
 struct StreamCfg {
   static constexpr int kRowPitch = TILES * 16 + 4;  // +4: a warp's fragment stores hit distinct banks
   static constexpr int kStepBytes = TILES * P::kBytes;
@@ -444,40 +444,46 @@ struct StreamCfg {
   static constexpr int kRed = WARPS * 8 * NT * kRowPitch;  // floats
   static constexpr int kRoom = (BLOCKS == 1 ? 227 : 113) * 1024;
   // Two buffers for the warps' sums, where they fit, save a barrier.
-  static constexpr int kReds = kRing + 2 * kRed * 4 <= kRoom ? 2 : 1;
+  static constexpr int kReds = CLUSTER == 1 && kRing + 2 * kRed * 4 <= kRoom ? 2 : 1;
   static constexpr int kSmem = kRing + kReds * kRed * 4;
   static_assert(kSmem <= kRoom, "shared memory budget");
+  static_assert(8 * NT * TILES * 16 * 4 <= kRing, "a block's sums fit where its ring was");
 };
 
 // P: the weights' policy.  MATS matrices, R row tiles of each a step, 8 * NT
 // rows of A, STAGES steps of the ring, WARPS a block, BLOCKS blocks an SM.
+// CLUSTER: blocks of a cluster that share one unit (where there are fewer units
+// than SMs to fill), each with every CLUSTER-th round of its steps; their sums
+// meet through distributed shared memory, in rank order.
 // SLOPES: dg and du of the gated product in place of it.
-template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES>
+template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, int CLUSTER, bool SLOPES>
 __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid_constant__ StreamParams p) {
-  constexpr int TILES = MATS * R;
-  using C = StreamCfg<P, TILES, NT, STAGES, WARPS, BLOCKS>;
+  constexpr int TILES = MATS * R, ALL = WARPS * CLUSTER;  // warps that share a unit's steps
+  using C = StreamCfg<P, TILES, NT, STAGES, WARPS, BLOCKS, CLUSTER>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem + C::kRing);
   [[maybe_unused]] float* sums = reinterpret_cast<float*>(smem + C::kSmem);  // A's, by step, group and row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CLUSTER > 1 ? (int)cluster_ctarank() : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, at = rank * WARPS + warp;
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * STAGES * C::kStepBytes);
-  // This block's run of units, one more or less than any other's.
-  const int first = (int)((int64_t)p.units * blockIdx.x / gridDim.x);
-  const int end = (int)((int64_t)p.units * (blockIdx.x + 1) / gridDim.x);
+  // This block's run of units, one more or less than any other's; one for a cluster.
+  const int mine = (int)blockIdx.x / CLUSTER, of = (int)gridDim.x / CLUSTER;
+  const int first = (int)((int64_t)p.units * mine / of);
+  const int end = (int)((int64_t)p.units * (mine + 1) / of);
   // The load cursor runs STAGES - 1 steps ahead of the compute cursor, across units.
-  int l_unit = warp < p.steps ? first : end;  // else nothing for this warp
-  int l_step = warp, l_slot = 0;
+  int l_unit = at < p.steps ? first : end;  // else nothing for this warp
+  int l_step = at, l_slot = 0;
   typename P::Cursor cursor;
-  if (l_unit < end) cursor.start(p, l_unit % p.groups * R, warp, lane);
+  if (l_unit < end) cursor.start(p, l_unit % p.groups * R, at, lane);
   auto fetch_next = [&]() {
     if (l_unit < end) {
       cursor.fetch(p, ring + (uint32_t)(l_slot * C::kStepBytes), lane);
-      l_step += WARPS;
+      l_step += ALL;
       if (l_step < p.steps) {
         cursor.advance(p);
       } else {
-        l_step = warp;
-        if (++l_unit < end) cursor.start(p, l_unit % p.groups * R, warp, lane);
+        l_step = at;
+        if (++l_unit < end) cursor.start(p, l_unit % p.groups * R, at, lane);
       }
       if (++l_slot == STAGES) l_slot = 0;
     }
@@ -495,13 +501,36 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
     pdl_wait();
   }
 
+  // Store a unit's outputs from its sums: value(m, column of the unit's tiles).
+  auto store = [&](int unit, auto value) {
+    const int chunk = unit / p.groups, tile = (unit - chunk * p.groups) * R, m0 = chunk * (8 * NT);
+    const int live = min(8 * NT, p.M - m0);
+    for (int x = rank * 32 * WARPS + threadIdx.x; x < live * R * 16; x += 32 * ALL) {
+      const int m = x / (R * 16), n = x % (R * 16);
+      const int64_t col = (int64_t)tile * 16 + n;
+      if (col >= p.N) continue;
+      float v[MATS];
+#pragma unroll
+      for (int a = 0; a < MATS; ++a) v[a] = value(m, a * R * 16 + n);
+      const int64_t to = (int64_t)(m0 + m) * p.ldc + col;
+      if constexpr (SLOPES) {
+        const uint16_t d16 = __ldg(p.dH + (int64_t)(m0 + m) * p.lddh + col);
+        const float d = P::FP16 ? __half2float(__ushort_as_half(d16)) : __bfloat162float(__ushort_as_bfloat16(d16));
+        const ActSlope s = act_of(v[0], p.act);
+        p.C[to] = round16<P::FP16>(d * v[MATS - 1] * s.slope);
+        p.C2[to] = round16<P::FP16>(d * s.value);
+      } else {
+        p.C[to] = round16<P::FP16>(MATS == 2 ? act_of(v[0], p.act).value * v[MATS - 1] : v[0]);
+      }
+    }
+  };
   int slot = 0, of_chunk = -1, red_at = 0;
   [[maybe_unused]] typename P::template Operand<NT> ahead;  // of the warp's next step, where registers allow
   for (int unit = first; unit < end; ++unit) {
-    const int chunk = unit / p.groups, tile = (unit - chunk * p.groups) * R;
+    const int chunk = unit / p.groups;
     const int m0 = chunk * (8 * NT);
     const bool same_rows = of_chunk == chunk;
-    const bool have = P::kSums > 0 && p.keep_sums && same_rows;
+    const bool have = P::kSums > 0 && CLUSTER == 1 && p.keep_sums && same_rows;
     of_chunk = chunk;
     const uint16_t* row[NT];  // rows past M repeat the last: their sums are not stored
 #pragma unroll
@@ -514,55 +543,57 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[r][t][e] = 0.0f;
 
-    if (P::template kAhead<NT> && !same_rows && warp < p.steps) ahead.load(p, row, warp, lane);
-    for (int step = warp; step < p.steps; step += WARPS) {
+    if (P::template kAhead<NT> && !same_rows && at < p.steps) ahead.load(p, row, at, lane);
+    for (int step = at; step < p.steps; step += ALL) {
       typename P::template Operand<NT> operand;
       if constexpr (P::template kAhead<NT>) {
         operand = ahead;
-        ahead.load(p, row, step + WARPS < p.steps ? step + WARPS : warp, lane);  // on to the next row tiles
+        ahead.load(p, row, step + ALL < p.steps ? step + ALL : at, lane);  // on to the next row tiles
       } else {
         operand.load(p, row, step, lane);
       }
       cp_async_wait<STAGES - 2>();
       if (P::kShared) __syncwarp();  // every lane's bytes are there, and the slot fetched into below has been read
-      float* kept = P::kSums > 0 && p.keep_sums ? sums + step * (P::kSums * 8 * NT) : nullptr;
+      float* kept = P::kSums > 0 && CLUSTER == 1 && p.keep_sums ? sums + step * (P::kSums * 8 * NT) : nullptr;
       P::template multiply<NT>(p, operand, step, ring + (uint32_t)(slot * C::kStepBytes), lane, kept, have, sum);
       fetch_next();  // into the slot that the step before this one read
       if (++slot == STAGES) slot = 0;
     }
 
     // The warps' sums, [warp][row of A][weight row], added in warp order.
-    float* mine = red + red_at + warp * 8 * NT * C::kRowPitch;
+    float* to_red = red + red_at + warp * 8 * NT * C::kRowPitch;
 #pragma unroll
     for (int r = 0; r < TILES; ++r)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          mine[(t * 8 + 2 * (lane & 3) + (e & 1)) * C::kRowPitch + r * 16 + (lane >> 2) + 8 * (e >> 1)] = sum[r][t][e];
+          to_red[(t * 8 + 2 * (lane & 3) + (e & 1)) * C::kRowPitch + r * 16 + (lane >> 2) + 8 * (e >> 1)] = sum[r][t][e];
     __syncthreads();
-    const int live = min(8 * NT, p.M - m0);
-    const int used = min(WARPS, p.steps);  // warps past that hold zeros
-    for (int x = threadIdx.x; x < live * R * 16; x += 32 * WARPS) {
-      const int m = x / (R * 16), n = x % (R * 16);
-      const int64_t col = (int64_t)tile * 16 + n;
-      if (col >= p.N) continue;
-      float v[MATS];
+    const int used = min(WARPS, p.steps - rank * WARPS);  // warps past that hold zeros
+    auto added = [&](int m, int n) {
+      float v = 0.0f;
+      for (int w = 0; w < used; ++w) v += red[red_at + (w * 8 * NT + m) * C::kRowPitch + n];
+      return v;
+    };
+    if constexpr (CLUSTER == 1) {
+      store(unit, added);
+    } else {
+      // this block's sums go where its ring was; each rank stores a share of the outputs
+      float* part = reinterpret_cast<float*>(smem);
+      const int live = min(8 * NT, p.M - m0);
+      for (int x = threadIdx.x; x < live * TILES * 16; x += 32 * WARPS)
+        part[x] = added(x / (TILES * 16), x % (TILES * 16));
+      cluster_sync_all();
+      store(unit, [&](int m, int n) {
+        float v = 0.0f;
 #pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        v[a] = 0.0f;
-        for (int w = 0; w < used; ++w) v[a] += red[red_at + (w * 8 * NT + m) * C::kRowPitch + a * R * 16 + n];
-      }
-      const int64_t to = (int64_t)(m0 + m) * p.ldc + col;
-      if constexpr (SLOPES) {
-        const uint16_t d16 = __ldg(p.dH + (int64_t)(m0 + m) * p.lddh + col);
-        const float d = P::FP16 ? __half2float(__ushort_as_half(d16)) : __bfloat162float(__ushort_as_bfloat16(d16));
-        const ActSlope s = act_of(v[0], p.act);
-        p.C[to] = round16<P::FP16>(d * v[MATS - 1] * s.slope);
-        p.C2[to] = round16<P::FP16>(d * s.value);
-      } else {
-        p.C[to] = round16<P::FP16>(MATS == 2 ? act_of(v[0], p.act).value * v[MATS - 1] : v[0]);
-      }
+        for (int r = 0; r < CLUSTER; ++r)
+          v += __uint_as_float(ld_shared_cluster_u32(
+              mapa_shared(smem_u32(part + m * (TILES * 16) + n), (uint32_t)r)));
+        return v;
+      });
+      cluster_sync_all();  // no block ends while its sums may still be read
     }
     // before the next sums replace these: with two buffers, the next barrier
     // lies between
@@ -574,10 +605,10 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS) stream_kernel(const __grid
   cp_async_wait<0>();
 }
 
-template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, bool SLOPES = false>
+template <class P, int MATS, int R, int NT, int STAGES, int WARPS, int BLOCKS, int CLUSTER = 1, bool SLOPES = false>
 int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
-  using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS, BLOCKS>;
-  auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS, SLOPES>;
+  using C = StreamCfg<P, MATS * R, NT, STAGES, WARPS, BLOCKS, CLUSTER>;
+  auto kern = stream_kernel<P, MATS, R, NT, STAGES, WARPS, BLOCKS, CLUSTER, SLOPES>;
   static std::atomic<bool> attr_set[64];
   if (const int rc = smem_attr_once(attr_set, kern, P::kSums > 0 ? C::kRoom : C::kSmem); rc != GP_OK) return rc;
   p.groups = (p.row_tiles + R - 1) / R;
@@ -585,19 +616,23 @@ int launch_stream(StreamParams p, int num_sms, cudaStream_t stream) {
   if (units > 0x40000000) return GP_ERR_SHAPE;  // more outputs than the memory holds
   p.units = (int)units;
   // A's sums are kept where a block has several units and they fit.
-  const int slots = BLOCKS * num_sms;
+  const int slots = BLOCKS * num_sms, clusters = CLUSTER > 1 || p.units < slots ? p.units : slots;
   const int64_t sums = (int64_t)p.steps * P::kSums * 8 * NT * 4;
-  p.keep_sums = P::kSums > 0 && units > slots && C::kSmem + sums <= C::kRoom ? 1 : 0;
+  p.keep_sums = P::kSums > 0 && units > clusters && C::kSmem + sums <= C::kRoom ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.units < slots ? p.units : slots));
+  cfg.gridDim = dim3((unsigned)(clusters * CLUSTER));
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = (size_t)(C::kSmem + (p.keep_sums ? sums : 0));
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CLUSTER;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return GP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
 }

@@ -82,6 +82,19 @@ def test_forward(M, N, K, dtype, act):
     assert untouched(out)
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 500, 4100), (11, 300, 3331), (30, 700, 5000), (60, 200, 4097)])
+def test_few_tokens_and_long_sums(M, N, K):
+    """Rows of weights too few to fill the GPU: four blocks share each 16."""
+    A, G, U, dH = operands(M, N, K, "bf16", seed=8)
+    first = gp.gated_matmul(A, G, U)
+    within(first, *ffn.gated_bound(f64(A), f64(G), f64(U), "silu", "bf16"))
+    for _ in range(10):
+        assert torch.equal(gp.gated_matmul(A, G, U, b_constant=True), first)
+    want, bounds = ffn.gated_backward_bound(f64(A), f64(G), f64(U), f64(dH), "silu", "bf16")
+    for o, w, b in zip(gp.gated_matmul_backward(A, G, U, dH), want, bounds):
+        within(o, w, b)
+
+
 BACKWARD = [(1, 1, 1), (1, 200, 72), (2, 64, 257), (5, 129, 65), (17, 130, 136), (64, 100, 300), (127, 257, 129),
             (128, 256, 256), (130, 65, 1030), (255, 511, 120), (257, 300, 257), (300, 1100, 64), (700, 129, 200),
             (1025, 72, 530)]

@@ -103,6 +103,30 @@ def test_gated_product(M, N, K, dtype, act, group, zeros):
     within(out, *ffn.w4g_bound(f64(A), [g, u], group, dtype, act))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 500, 8192), (3, 1200, 4128), (12, 1100, 4256), (1, 2000, 2080), (8, 2400, 4096),
+                                   (15, 1700, 2592), (40, 380, 5120)])
+@pytest.mark.parametrize("dtype,group,zeros", [("bf16", 128, True), ("fp16", 32, False)])
+def test_few_columns_and_long_sums(M, N, K, dtype, group, zeros):
+    """Row tiles too few to fill the GPU: two or four blocks share each."""
+    w, W = make(N, K, group, zeros, dtype, seed=10)
+    u, U = make(N, K, group, zeros, dtype, seed=11)
+    A = activations(M, K, dtype, seed=10)
+    within(gp.matmul_w4g(A, W), *ffn.w4g_bound(f64(A), [w], group, dtype))
+    first = gp.matmul_w4g_gated(A, W, U)
+    within(first, *ffn.w4g_bound(f64(A), [w, u], group, dtype, "silu"))
+    for _ in range(10):
+        assert torch.equal(gp.matmul_w4g_gated(A, W, U, b_constant=True), first)
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 15000, 256), (20, 8000, 160), (8, 20000, 128)])
+def test_many_columns(M, N, K):
+    """Several units a block, in each of the forms that many row tiles take."""
+    for group, dtype in ((128, "bf16"), (64, "fp16")):
+        w, W = make(N, K, group, True, dtype, seed=12)
+        A = activations(M, K, dtype, seed=12)
+        within(gp.matmul_w4g(A, W), *ffn.w4g_bound(f64(A), [w], group, dtype))
+
+
 def test_offset_codes_cancel():
     """A constant activation: the offset's share of the sum is thirty times the result."""
     N, K, group = 64, 2048, 128
