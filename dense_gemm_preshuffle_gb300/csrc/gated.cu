@@ -64,11 +64,29 @@ Parts parts_of(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-// dg | du | INPUT's fp32 parts | WEIGHTS' fp32 parts
+// The same for SLOPES alone, whose parts hold two sums; the launch that joins
+// them computes more.  300 x 500 x 4000 whole and in the 8 parts that it takes,
+// all of the backward pass: 36.5 and 27.0 us; 1000 x 512 x 1024 is left whole,
+// 22.3 us, and would take 24.3 with 4.
+int slope_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = cdiv(M, 256) * cdiv(N, 128), k = cdiv(K, 64);
+  int best = 1;
+  double best_us = 0.0;
+  for (int p : {1, 2, 3, 4, 6, 8}) {
+    if (p > 1 && p * 4 > k) break;
+    double us = 0.36 * (double)(cdiv(tiles * p, kPairs) * tile_steps(k, p));
+    if (p > 1) us += 4.5 + 16.0 * (double)p * (double)M * (double)N / 12.0e6;
+    if (p == 1 || us < best_us) best = p, best_us = us;
+  }
+  return best;
+}
+
+// dg | du | SLOPES' fp32 parts, or later INPUT's and WEIGHTS'
 struct Workspace {
   Parts parts;
+  int slopes;          // parts
   int64_t pitch;       // of dg and du, in elements
-  int64_t part_pitch;  // of the fp32 parts
+  int64_t part_pitch;  // of INPUT's and WEIGHTS' fp32 parts; SLOPES' have dg's
   int64_t du, input, weights, bytes;
 };
 Workspace workspace_of(int64_t M, int64_t N, int64_t K) {
@@ -80,6 +98,8 @@ Workspace workspace_of(int64_t M, int64_t N, int64_t K) {
   w.input = 2 * w.du;
   w.weights = w.input + (w.parts.input > 1 ? w.parts.input * M * w.part_pitch * 4 : 0);
   w.bytes = w.weights + (w.parts.weights > 1 ? 2 * w.parts.weights * N * w.part_pitch * 4 : 0);
+  w.slopes = slope_parts(M, N, K);
+  if (w.slopes > 1) w.bytes = std::max(w.bytes, w.input + 2 * w.slopes * M * w.pitch * 4);
   return w;
 }
 
@@ -143,14 +163,14 @@ int set_product(GatedProduct& g, int64_t outputs, int64_t parts, int64_t rows, i
   return GP_OK;
 }
 
-// FORWARD, or SLOPES where dH is given.
-int products_launch(const GatedArgs& a, const HostContext& ctx, const Matrix& out0, const Matrix& out1,
-                    cudaStream_t stream) {
+// FORWARD, or SLOPES where dH is given, in `parts` with fp32 sums in `partial`.
+int products_launch(const GatedArgs& a, const HostContext& ctx, const Matrix& out0, const Matrix& out1, int parts,
+                    float* partial, cudaStream_t stream) {
   const int mode = a.dH != nullptr ? GATED_SLOPES : GATED_FORWARD;
   GatedMaps maps{};
   GatedPairParams p = params_of(a, ctx);
   p.b_constant = a.b_constant ? 1 : 0;
-  if (const int rc = set_product(p.product[0], 1, 1, a.M, a.N, 128, cdiv(a.K, 64), ctx.l2_bytes); rc != GP_OK)
+  if (const int rc = set_product(p.product[0], 1, parts, a.M, a.N, 128, cdiv(a.K, 64), ctx.l2_bytes); rc != GP_OK)
     return rc;
   Encoder e{a.fp16};
   e.map16(&maps.a[0], {a.A, a.M, a.K, a.lda}, 128);
@@ -162,9 +182,21 @@ int products_launch(const GatedArgs& a, const HostContext& ctx, const Matrix& ou
     e.map16(&maps.c[0], out0, 32);
     e.map16(&maps.c[1], out1, 32);
     e.map16(&maps.dh, {a.dH, a.M, a.N, a.lddh}, 32);
+    if (parts > 1) e.parts(&maps.partial[0], partial, 2 * parts, a.M, a.N, out0.ld);
   }
   if (e.rc != GP_OK) return e.rc;
-  return gated_pair_launch(mode, maps, p, ctx.num_sms, stream);
+  const int rc = gated_pair_launch(mode, maps, p, ctx.num_sms, stream);
+  if (rc != GP_OK || parts == 1) return rc;
+  GatedSlopeParts s{};
+  s.partial = partial;
+  s.parts = parts;
+  s.rows = a.M, s.cols = a.N, s.pitch = out0.ld;
+  s.dh = static_cast<const uint16_t*>(a.dH);
+  s.lddh = a.lddh;
+  s.dg = static_cast<uint16_t*>(const_cast<void*>(out0.p));
+  s.du = static_cast<uint16_t*>(const_cast<void*>(out1.p));
+  s.ld = out0.ld;
+  return gated_slope_parts_launch(s, a.act, a.fp16, ctx.num_sms, stream);
 }
 
 }  // namespace
@@ -173,7 +205,7 @@ size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K) { return (size_t)w
 
 int gated_run_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
   if (gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)) return gated_stream_launch(a, a.H, nullptr, a.ldh, ctx, stream);
-  return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, stream);
+  return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, 1, nullptr, stream);
 }
 
 int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
@@ -184,7 +216,7 @@ int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream
   float *input_parts = reinterpret_cast<float*>(ws + w.input), *weight_parts = reinterpret_cast<float*>(ws + w.weights);
   int rc = gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)
                ? gated_stream_launch(a, ws, ws + w.du, w.pitch, ctx, stream)
-               : products_launch(a, ctx, dg, du, stream);
+               : products_launch(a, ctx, dg, du, w.slopes, input_parts, stream);
   if (rc != GP_OK) return rc;
 
   GatedMaps maps{};

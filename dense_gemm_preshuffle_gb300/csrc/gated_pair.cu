@@ -28,9 +28,9 @@
 // Two accumulators (512 TMEM columns) let each tile's epilogue run beside the
 // next tile's MMAs.  GRADIENTS takes INPUT's tiles first, which are long, and
 // fills the pairs that have fewer of them with more of WEIGHTS' (see tile_of).
-// A product of few tiles and a long reduction is split along it: each part
-// writes fp32 sums to the workspace and a second kernel adds them in order, so
-// results do not depend on timing.
+// A product of few tiles and a long reduction is split along it (SLOPES,
+// INPUT, WEIGHTS): each part writes fp32 sums to the workspace and a second
+// kernel adds them in order, so results do not depend on timing.
 //
 // Roles as in gemm_pair.cu: warp 0 copies (lane 0 B, lane 1 A), warp 1 issues
 // the MMAs in the even CTA, warps 2-9 are the epilogue, two for each TMEM
@@ -105,6 +105,13 @@ __device__ __forceinline__ void stage_row(uint32_t row_addr, int lane, int h, co
   for (int q = 0; q < 4; ++q)
     st_shared_v4(row_addr + (uint32_t)((((h * 4 + q) ^ (lane & 7)) * 16)), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2],
                  pk[4 * q + 3]);
+}
+
+// A row's 32 fp32 columns of a 32 x 32 staging tile, in the same swizzle.
+__device__ __forceinline__ void stage_fp32(uint32_t row_addr, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    st_shared_v4(row_addr + (uint32_t)(((q ^ (lane & 7)) * 16)), r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
 }
 
 // The columns of a row's 32 (from column n) that lie in [tail, cols).
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         // This warp's dH tile, requested while the tile's MMAs still run,
         // into the staging tile that dg will leave from.
         const int n0 = a.nb * 128 + chalf * 64;
-        dh_wanted = row0 < g.rows && n0 < g.cols;
+        dh_wanted = g.parts == 1 && row0 < g.rows && n0 < g.cols;
         if (lane == 0) bulk_wait_group_read<0>();  // the previous stores have read the staging tiles
         if (dh_wanted && lane == 0) {
           mbar_arrive_expect_tx(dhb, 4096);
@@ -406,6 +413,23 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acce_leader + (uint32_t)(buf * 8));
           }
+          if (MODE == GATED_SLOPES && g.parts > 1) {
+            // fp32 sums of this part, of g and of u: 32 x 32 tiles, 128 bytes a row
+            if (h == 1) {
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+            }
+            stage_fp32(stg_row, lane, gr);
+            stage_fp32(stg_row + 4096, lane, ur);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < g.rows && n0 + h * 32 < g.cols) {
+              tma_store_3d(&maps.partial[0], n0 + h * 32, row0, 2 * a.part, stg);
+              tma_store_3d(&maps.partial[0], n0 + h * 32, row0, 2 * a.part + 1, stg2);
+              bulk_commit_group();
+            }
+            continue;
+          }
           if constexpr (MODE == GATED_SLOPES) {
             uint32_t d[16], dg[16], du[16];
 #pragma unroll
@@ -430,6 +454,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             store_tail(p, g, 0, row0 + lane, n0 + h * 32, pk);
           }
         }
+        if (MODE == GATED_SLOPES && g.parts > 1) continue;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && inside) {
@@ -457,10 +482,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
               // fp32 sums of this part: a 32 x 32 tile, 128 bytes a row
               if (lane == 0) bulk_wait_group_read<0>();
               __syncwarp();
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                st_shared_v4(stg_row + (uint32_t)(((q ^ (lane & 7)) * 16)), r[4 * q], r[4 * q + 1], r[4 * q + 2],
-                             r[4 * q + 3]);
+              stage_fp32(stg_row, lane, r);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0 && row0 < g.rows && n0 + h * 32 < g.cols) {
@@ -534,6 +556,46 @@ __global__ void __launch_bounds__(256) gated_add_parts_kernel(const __grid_const
   }
 }
 
+// dg and du from the parts' fp32 sums of g and u, [part][g, u][rows][pitch].
+template <int ACT>
+__global__ void __launch_bounds__(256) gated_slope_parts_kernel(const __grid_constant__ GatedSlopeParts p, int fp16) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const float4* partial = reinterpret_cast<const float4*>(p.partial);
+  const int64_t quads = p.pitch / 4, plane = p.rows * quads;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < plane; x += step) {
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.parts; ++s) {
+      const float4 a = partial[(2 * s) * plane + x], b = partial[(2 * s + 1) * plane + x];
+      g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w;
+      u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+    }
+    const int64_t r = x / quads, c = (x - r * quads) * 4;
+    const uint16_t* dh = p.dh + r * p.lddh + c;
+    uint16_t d[4];
+    if (c + 4 <= p.cols) {  // rows start on 16-byte boundaries, c on a multiple of 4
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(dh));
+      d[0] = (uint16_t)v.x, d[1] = (uint16_t)(v.x >> 16), d[2] = (uint16_t)v.y, d[3] = (uint16_t)(v.y >> 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = c + e < p.cols ? __ldg(dh + e) : (uint16_t)0;
+    }
+    uint32_t dg[2], du[2];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float2 h = unpack16((uint32_t)d[e] | (uint32_t)d[e + 1] << 16, fp16 != 0);
+      const ActSlope lo = act_slope<ACT>(g[e]), hi = act_slope<ACT>(g[e + 1]);
+      const float g0 = h.x * u[e] * lo.slope, g1 = h.y * u[e + 1] * hi.slope, u0 = h.x * lo.value, u1 = h.y * hi.value;
+      dg[e / 2] = fp16 ? pack_f16x2(g0, g1) : pack_bf16x2(g0, g1);
+      du[e / 2] = fp16 ? pack_f16x2(u0, u1) : pack_bf16x2(u0, u1);
+    }
+    // into the workspace, whose rows have room for whole quads
+    *reinterpret_cast<uint2*>(p.dg + r * p.ld + c) = make_uint2(dg[0], dg[1]);
+    *reinterpret_cast<uint2*>(p.du + r * p.ld + c) = make_uint2(du[0], du[1]);
+  }
+}
+
 template <int MODE>
 int launch_mode(const GatedMaps& maps, GatedPairParams p, int num_sms, cudaStream_t stream) {
   using C = Cfg<MODE>;
@@ -570,12 +632,13 @@ int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p,
   }
 }
 
-int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int num_sms, cudaStream_t stream) {
-  int64_t most = 0;
-  for (int i = 0; i < count; ++i) most = std::max(most, list.of[i].rows * list.of[i].pitch / 4);
-  const int64_t blocks = std::min<int64_t>((most + 255) / 256, (int64_t)num_sms * 8);
+namespace {
+
+// A grid-stride kernel over `items` threads' work, beside the end of the one before it.
+template <typename Kern, typename... Args>
+int launch_over(Kern kern, int64_t items, int count, int num_sms, cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)count);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((items + 255) / 256, (int64_t)num_sms * 8), (unsigned)count);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -583,8 +646,23 @@ int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gated_add_parts_kernel, list, fp16 ? 1 : 0) != cudaSuccess) return GP_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return GP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
+}
+
+}  // namespace
+
+int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int num_sms, cudaStream_t stream) {
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) most = std::max(most, list.of[i].rows * list.of[i].pitch / 4);
+  return launch_over(gated_add_parts_kernel, most, count, num_sms, stream, list, fp16 ? 1 : 0);
+}
+
+int gated_slope_parts_launch(const GatedSlopeParts& p, int act, bool fp16, int num_sms, cudaStream_t stream) {
+  auto kern = act == GP_ACT_RELU   ? gated_slope_parts_kernel<GP_ACT_RELU>
+              : act == GP_ACT_SILU ? gated_slope_parts_kernel<GP_ACT_SILU>
+                                   : gated_slope_parts_kernel<GP_ACT_GELU>;
+  return launch_over(kern, p.rows * p.pitch / 4, 1, num_sms, stream, p, fp16 ? 1 : 0);
 }
 
 }  // namespace gp

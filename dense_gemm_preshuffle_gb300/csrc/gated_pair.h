@@ -15,7 +15,8 @@ struct GatedMaps {
   CUtensorMap wa[2], wb;   // WEIGHTS: dg, du and the activation, MN-major
   CUtensorMap c[3];        // the outputs; GRADIENTS: dA, dG, dU
   CUtensorMap dh;          // SLOPES
-  CUtensorMap partial[2];  // GRADIENTS: INPUT's and WEIGHTS' parts, [outputs * parts][rows][pitch] fp32
+  CUtensorMap partial[2];  // INPUT's (or SLOPES') and WEIGHTS' parts, [outputs * parts][rows][pitch] fp32;
+                           // SLOPES has two sums a part, g and u
 };
 
 // One product of a launch: FORWARD, SLOPES and INPUT are product 0, WEIGHTS,
@@ -58,6 +59,18 @@ struct GatedPartsList {
   GatedParts of[3];
 };
 int gated_add_parts_launch(const GatedPartsList& list, int count, bool fp16, int num_sms, cudaStream_t stream);
+
+// dg and du from the parts of g and u, and dH.
+struct GatedSlopeParts {
+  const float* partial;  // [parts][2][rows][pitch]
+  int parts;
+  int64_t rows, cols, pitch;
+  const uint16_t* dh;
+  int64_t lddh;
+  uint16_t *dg, *du;
+  int64_t ld;
+};
+int gated_slope_parts_launch(const GatedSlopeParts& p, int act, bool fp16, int num_sms, cudaStream_t stream);
 
 // FORWARD and SLOPES for few tokens or little work (gated_stream.cu): whether
 // it takes them, and the launch, into out0 (and out1 for SLOPES) of pitch ld.

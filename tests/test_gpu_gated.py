@@ -115,6 +115,18 @@ def test_backward(M, N, K, dtype, act):
     assert bool((ws[nbytes:] == 255).all())  # nothing past the stated size
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 500, 4000), (260, 1001, 1100), (520, 196, 2111), (129, 2, 5000)])
+@pytest.mark.parametrize("dtype,act", [("bf16", "silu"), ("fp16", "gelu"), ("bf16", "relu")])
+def test_backward_long_sums(M, N, K, dtype, act):
+    """Few tiles and a long sum: the gates' own products are split along it too."""
+    test_backward(M, N, K, dtype, act)
+    operand = operands(M, N, K, dtype, seed=1)
+    first = gp.gated_matmul_backward(*operand, act=act)
+    for need in ({}, {"need_dA": False}, {"need_dW": False}):
+        again = gp.gated_matmul_backward(*operand, act=act, **need)
+        assert all(x is None or torch.equal(x, y) for x, y in zip(again, first))
+
+
 @pytest.mark.parametrize("need_dA,need_dW", [(True, False), (False, True)])
 def test_backward_in_parts(need_dA, need_dW):
     A, G, U, dH = operands(70, 190, 130, "bf16", seed=2)
