@@ -1,0 +1,589 @@
+// Products with 4-bit group-scaled weights on the tensor cores' tiles:
+//
+//   C[m, n] = sum over groups j of s[n, j] * sum_{k in j} (q[n, k] - z[n, j]) A[m, k]
+//
+// for more rows of A than the streaming kernel's, each of whose units reads
+// all of them again beside 16 rows of weights.  Here a unit is 128 rows of
+// weights (64 of each matrix for a gated product) and T rows of A.
+//   - The weights are the MMA's 128-row operand, in tensor memory: a warp
+//     decodes a block of 16 rows x 128 values into (q - z) as 16-bit floats,
+//     which are exact, and stores them with the lanes of its MMA fragments
+//     (tcgen05.st 16x128b); they never go through shared memory decoded.
+//     q - z takes no arithmetic but one subtraction: a code is put into the
+//     low bits of 128's (bf16) or 1024's (fp16) fraction.
+//   - A's rows are the MMA's T columns, by TMA.  In a packed word four lanes
+//     hold 8 consecutive values each where the fragments have pairs in turn,
+//     so two warps transpose the 4 x 4 words of every 64 bytes of A in place;
+//     the sum does not change when both operands are permuted alike.
+//   - Every group is an accumulator of its own (a ring of them in tensor
+//     memory).  The drain warps, a weight row to a thread, multiply it by the
+//     group's scale and add it in fp32 registers.
+//   - Few units: a cluster of CTAs shares one unit's groups, and its sums meet
+//     through distributed shared memory in rank order.
+// Roles: drain, decode, one warp each for the MMAs, the copies of the weights
+// and of A, and A's transposition.  Every wait is bounded.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "gated_math.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "w4g.h"
+
+namespace gp {
+
+namespace {
+
+constexpr int TW_BLOCKS = 2;  // blocks of 128 values a step: each hand-over among the roles covers 256
+
+template <int GROUP, int T>
+struct TileCfg {
+  static constexpr int kGroups = 128 / GROUP * TW_BLOCKS;  // of a step
+  static constexpr int kHalf =  // room for four row tiles' blocks of a step
+      (4 * TW_BLOCKS * (1024 + 48 * (128 / GROUP)) + 127) / 128 * 128;
+  static constexpr int kCols = 32;                    // columns of a drain warp
+  static constexpr int kDrain = 4 * (T / kCols);      // warps that drain a group
+  static constexpr int kDrainSets = T == 32 ? 2 : 1;  // groups drained at once
+  static constexpr int kSets = T == 32 ? 2 : 1;       // steps decoded at once, by 8 warps each
+  static constexpr int kIssuers = 2;                  // warps that issue MMAs, a group each in turn
+  static constexpr int kPermute = T == 32 ? 4 : 8;
+  static constexpr int kDecode0 = kDrain * kDrainSets, kMma0 = kDecode0 + 8 * kSets, kCodes = kMma0 + kIssuers,
+                       kTokens = kCodes + 1, kPermute0 = kTokens + 1, kWarps = kPermute0 + kPermute;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = T == 32 ? 6 : 4;   // ring of weight blocks, in steps
+  static constexpr int kTokBufs = T == 32 ? 4 : 3;  // of A's rows
+  static constexpr int kABufs = 2;                  // decoded steps in tensor memory
+  static constexpr int kACols = 64 * TW_BLOCKS;
+  static constexpr int kDBufs = 256 / T;                 // groups' accumulators in tensor memory
+  static constexpr int kTokBytes = TW_BLOCKS * T * 256;  // panels of T rows x 64 values
+  static constexpr int kRing = kStages * 2 * kHalf;
+  static constexpr int kOut = T * 128 * 4;  // the unit's sums
+  static constexpr int kBars = 2 * kStages + 3 * kTokBufs + 2 * kABufs + 2 * kDBufs + kIssuers;
+  static constexpr int kSmem = kTokBufs * kTokBytes + kRing + kOut + 512 + 1024;
+  static_assert(kBars * 8 + 8 <= 512 && kSmem <= 232448, "shared memory budget");
+  static_assert(kThreads <= 1024, "threads of a block");
+  // Who waits on a buffer in turn with others might take an earlier pass's
+  // parity for its own: each buffer has one set of warps, or every one visits it.
+  static_assert(kDBufs % kIssuers == 0 && kDBufs % kDrainSets == 0, "an accumulator has one issuer and one drain set");
+  static_assert(kABufs % kSets == 0 && kStages % kSets == 0, "a buffer of decoded weights has one decode set");
+  static_assert(kGroups % kIssuers == 0, "an issuer takes part in every step");
+  static_assert(kABufs * kACols + kDBufs * T <= 512, "tensor memory");
+};
+
+// A position in a ring of N buffers and the parity of its pass.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void advance(int by) {
+    i += by;
+    if (i >= N) {
+      i -= N;
+      ph ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_half(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// 32 columns of 16 lanes: register 2r holds row l / 4, column 4r + l % 4, and
+// register 2r + 1 the same of row l / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] . B[smem]^T, 16-bit operands, one thread issues.
+__device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// Codes 2J and 2J + 1 of a packed word, minus z, as a pair of 16-bit floats.
+// z: 128 + z as bf16; for fp16 1024 + z where J is even and -(64 + z) where it
+// is odd, which takes bits 4-7 without a shift: 1024 + 16 q, divided by 16.
+template <bool FP16, int J>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t magic, uint32_t z) {
+  uint32_t v, r;
+  if constexpr (!FP16) {
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w >> (4 * J)), "r"(magic));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z));
+  } else if constexpr (J % 2 == 0) {
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w >> (4 * J)), "r"(magic));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z));
+  } else {
+    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(v) : "r"(w >> (4 * J - 4)), "r"(magic));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x2C002C00u), "r"(z));
+  }
+  return r;
+}
+// The even codes' z to the odd ones', fp16: -(64 + z) = 960 - (1024 + z).
+template <bool FP16>
+__device__ __forceinline__ uint32_t odd_zero(uint32_t z) {
+  if constexpr (!FP16) return z;
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(0x63806380u), "r"(z));
+  return r;
+}
+
+__device__ __forceinline__ float gate_of(float g, float u, int act) {
+  switch (act) {
+    case GP_ACT_RELU: return act_value<GP_ACT_RELU>(g) * u;
+    case GP_ACT_SILU: return act_value<GP_ACT_SILU>(g) * u;
+    default: return act_value<GP_ACT_GELU>(g) * u;
+  }
+}
+template <bool FP16>
+__device__ __forceinline__ uint16_t to16(float v) {
+  return (uint16_t)(FP16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
+}
+
+// A whole warp's wait: every lane returns the same.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          const W4gTileParams& p, uint32_t why) {
+  bool ok = false;
+  for (int i = 0; !ok && i < 16; ++i) ok = mbar_try_wait(bar, parity);
+  return __all_sync(0xFFFFFFFFu, ok || wait_bounded(bar, parity, abort_flag, p.status, why, p.wait_limit_ns));
+}
+
+template <bool FP16, int GROUP, int T>
+__global__ void __launch_bounds__(TileCfg<GROUP, T>::kThreads, 1)
+    w4g_tile_kernel(const __grid_constant__ W4gTileMaps maps, const __grid_constant__ W4gTileParams p) {
+  using C = TileCfg<GROUP, T>;
+  constexpr int COLS = C::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_tok = base;
+  uint8_t* s_ring = s_tok + C::kTokBufs * C::kTokBytes;
+  float* s_out = reinterpret_cast<float*>(s_ring + C::kRing);  // [T][128]
+  uint64_t* codes_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_out) + C::kOut);
+  uint64_t* codes_empty = codes_full + C::kStages;
+  uint64_t* tok_full = codes_empty + C::kStages;
+  uint64_t* tok_ready = tok_full + C::kTokBufs;
+  uint64_t* tok_empty = tok_ready + C::kTokBufs;
+  uint64_t* a_full = tok_empty + C::kTokBufs;
+  uint64_t* a_empty = a_full + C::kABufs;
+  uint64_t* d_full = a_empty + C::kABufs;
+  uint64_t* d_empty = d_full + C::kDBufs;
+  uint64_t* drained = d_empty + C::kDBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + C::kIssuers);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = p.wait_limit_ns;
+  const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&codes_full[s], 1);
+      mbar_init(&codes_empty[s], 8 + C::kDrain * C::kDrainSets);
+    }
+    for (int s = 0; s < C::kTokBufs; ++s) {
+      mbar_init(&tok_full[s], 1);
+      mbar_init(&tok_ready[s], C::kPermute);
+      mbar_init(&tok_empty[s], C::kIssuers);
+    }
+    for (int s = 0; s < C::kABufs; ++s) {
+      mbar_init(&a_full[s], 8);
+      mbar_init(&a_empty[s], C::kIssuers);
+    }
+    for (int s = 0; s < C::kDBufs; ++s) {
+      mbar_init(&d_full[s], 1);
+      mbar_init(&d_empty[s], C::kDrain);
+    }
+    for (int s = 0; s < C::kIssuers; ++s) mbar_init(&drained[s], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == C::kMma0) tmem_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_d = tmem + C::kABufs * C::kACols;
+
+  // This CTA's run of units, and its part of each one's steps.
+  const int mine = (int)blockIdx.x / p.cluster, of = (int)gridDim.x / p.cluster;
+  const int first = (int)((int64_t)p.units * mine / of), end = (int)((int64_t)p.units * (mine + 1) / of);
+  const int all_steps = (p.kblocks + TW_BLOCKS - 1) / TW_BLOCKS;
+  const int c0 = (int)((int64_t)all_steps * rank / p.cluster), c1 = (int)((int64_t)all_steps * (rank + 1) / p.cluster);
+  const int steps = (end - first) * (c1 - c0);  // the host bounds it
+
+  pdl_launch_dependents();
+  if (!(warp == C::kCodes && p.b_constant)) pdl_wait();
+
+  if (warp == C::kCodes) {
+    // ------------------------------------------------------------ weights
+    if (lane == 0) {
+      Ring<C::kStages> st;
+      int it = 0;
+      bool ok = true;
+      for (int unit = first; ok && unit < end; ++unit) {
+        const int row = unit % p.tiles * (p.gated ? 4 : 8);
+        for (int c = c0; c < c1; ++c, ++it, st.advance(1)) {
+          if (!wait_bounded(&codes_empty[st.i], st.ph ^ 1, abort_flag, p.status, ST_TIMEOUT_PRODUCER, limit)) {
+            ok = false;
+            break;
+          }
+          // Fault injection (host-selected): a stage without its copies.
+          if (p.debug_skip_load == 1 + it) continue;
+          mbar_arrive_expect_tx(&codes_full[st.i], (uint32_t)(8 * TW_BLOCKS * p.block_bytes));
+          uint8_t* dst = s_ring + st.i * 2 * C::kHalf;
+          tma_load_3d(dst, &maps.w, 0, c * TW_BLOCKS, row, &codes_full[st.i]);
+          tma_load_3d(dst + C::kHalf, p.gated ? &maps.u : &maps.w, 0, c * TW_BLOCKS, p.gated ? row : row + 4,
+                      &codes_full[st.i]);
+        }
+      }
+      if (!ok || *abort_flag) {  // nothing lands after the exit
+        for (int i = 1; i <= min(it, C::kStages); ++i) {
+          const int q = it - i;
+          volatile int never = 0;
+          if (p.debug_skip_load == 1 + q) continue;
+          wait_bounded(&codes_full[q % C::kStages], (uint32_t)(q / C::kStages) & 1, &never, p.status, ST_TIMEOUT_DRAIN,
+                       limit);
+        }
+      }
+    }
+  } else if (warp == C::kTokens) {
+    // ------------------------------------------------------------ rows of A
+    if (lane == 0) {
+      Ring<C::kTokBufs> tb;
+      int it = 0;
+      bool ok = true;
+      for (int unit = first; ok && unit < end; ++unit) {
+        const int m0 = unit / p.tiles * T;
+        for (int c = c0; c < c1; ++c, ++it, tb.advance(1)) {
+          if (!wait_bounded(&tok_empty[tb.i], tb.ph ^ 1, abort_flag, p.status, ST_TIMEOUT_PRODUCER, limit)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&tok_full[tb.i], (uint32_t)C::kTokBytes);
+          uint8_t* dst = s_tok + tb.i * C::kTokBytes;
+#pragma unroll
+          for (int x = 0; x < 2 * TW_BLOCKS; ++x)
+            tma_load_2d(dst + x * (T * 128), &maps.a, (c * 2 * TW_BLOCKS + x) * 64, m0, &tok_full[tb.i]);
+        }
+      }
+      if (!ok || *abort_flag) {
+        for (int i = 1; i <= min(it, C::kTokBufs); ++i) {
+          const int q = it - i;
+          volatile int never = 0;
+          wait_bounded(&tok_full[q % C::kTokBufs], (uint32_t)(q / C::kTokBufs) & 1, &never, p.status, ST_TIMEOUT_DRAIN,
+                       limit);
+        }
+      }
+    }
+  } else if (warp >= C::kPermute0) {
+    // ------------------------------------------------------------ A's words
+    const int g = lane >> 2, t = lane & 3;
+    Ring<C::kTokBufs> tb;
+    bool ok = true;
+    for (int unit = first; ok && unit < end; ++unit) {
+      const int live = min(T, p.M - unit / p.tiles * T);     // the rows past it are zeros
+      const int tasks = (live + 7) / 8 * (2 * TW_BLOCKS);    // 8 rows x 64 values
+      for (int c = c0; c < c1; ++c, tb.advance(1)) {
+        ok = wait_warp(&tok_full[tb.i], tb.ph, abort_flag, p, ST_TIMEOUT_CONSUMER);
+        if (!ok) break;
+        const uint32_t tok = smem_u32(s_tok + tb.i * C::kTokBytes);
+#pragma unroll 4
+        for (int x = warp - C::kPermute0; x < tasks; x += C::kPermute) {
+          const uint32_t row = tok + (uint32_t)((x % (2 * TW_BLOCKS)) * (T * 128) + (x / (2 * TW_BLOCKS) * 8 + g) * 128);
+          const uint4 a = lds_v4(row + (uint32_t)((t ^ g) * 16)), b = lds_v4(row + (uint32_t)(((4 + t) ^ g) * 16));
+          __syncwarp();  // the 64 bytes are read before any lane writes them
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sts_word(row + (uint32_t)((j ^ g) * 16 + t * 4), aw[j]);
+            sts_word(row + (uint32_t)(((4 + j) ^ g) * 16 + t * 4), bw[j]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tok_ready[tb.i]);
+      }
+    }
+  } else if (warp >= C::kMma0) {
+    // ------------------------------------------------------------ MMAs
+    // The whole warp runs the loop and one lane issues: the operands' addresses
+    // stay in uniform registers, which the instructions take.
+    constexpr uint32_t idesc = idesc_dense(FP16 ? 0u : 1u, FP16 ? 0u : 1u, 128, T);
+    const int issuer = __shfl_sync(0xFFFFFFFFu, warp - C::kMma0, 0);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    bool ok = true;
+    Ring<C::kABufs> ab;
+    Ring<C::kTokBufs> tb;
+    for (int it = 0; ok && it < steps; ++it, ab.advance(1), tb.advance(1)) {
+      ok = wait_warp(&a_full[ab.i], ab.ph, abort_flag, p, ST_TIMEOUT_MMA) &&
+           wait_warp(&tok_ready[tb.i], tb.ph, abort_flag, p, ST_TIMEOUT_MMA);
+      if (!ok) break;
+      const uint64_t bdesc = smem_desc_sw128(smem_u32(s_tok + tb.i * C::kTokBytes));
+      const uint32_t a_at = tm + (uint32_t)(ab.i * C::kACols);
+#pragma unroll
+      for (int x = 0; x < C::kGroups / C::kIssuers; ++x) {
+        const int j = x * C::kIssuers + issuer, d = it * C::kGroups + j, db = d % C::kDBufs;
+        ok = wait_warp(&d_empty[db], ((uint32_t)(d / C::kDBufs) & 1) ^ 1, abort_flag, p, ST_TIMEOUT_MMA);
+        if (!ok) break;
+        tc_fence_after();
+        // 16 values: 8 columns of the decoded weights, 32 bytes of A's rows
+        const uint64_t bj = bdesc + (uint64_t)((j * GROUP / 64 * (T * 128) + j * GROUP % 64 * 2) >> 4);
+        const uint32_t aj = a_at + (uint32_t)(j * (GROUP / 2)), dj = tm + (uint32_t)(C::kABufs * C::kACols + db * T);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < GROUP / 16; ++i)
+            umma_tmem_a(dj, aj + (uint32_t)(i * 8), bj + (uint64_t)(((i >> 2) * (T * 128) + (i & 3) * 32) >> 4), idesc,
+                        i > 0 ? 1u : 0u);
+          umma_commit(&d_full[db]);
+          if (x == C::kGroups / C::kIssuers - 1) {
+            umma_commit(&a_empty[ab.i]);
+            umma_commit(&tok_empty[tb.i]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // Every issued MMA must complete before tensor memory is released.
+    if (elect_one()) {
+      uint64_t* done = drained + issuer;
+      umma_commit(done);
+      volatile int never = 0;
+      wait_bounded(done, 0, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+    }
+  } else if (warp >= C::kDecode0) {
+    // ------------------------------------------------------------ decode
+    const int quad = warp & 3, sub = ((warp - C::kDecode0) >> 2) & 1, set = (warp - C::kDecode0) >> 3;
+    const int block = 2 * quad + sub, g = lane >> 2;
+    const uint32_t at = tmem + ((uint32_t)(quad * 32 + sub * 16) << 16);
+    uint32_t magic;  // a register: a second constant would make the and-or two instructions
+    asm("mov.b32 %0, %1;" : "=r"(magic) : "n"(FP16 ? 0x64006400u : 0x43004300u));
+    Ring<C::kStages> st;
+    Ring<C::kABufs> ab;
+    st.advance(set);
+    ab.advance(set);
+    for (int it = set; it < steps; it += C::kSets, st.advance(C::kSets), ab.advance(C::kSets)) {
+      if (!wait_warp(&codes_full[st.i], st.ph, abort_flag, p, ST_TIMEOUT_CONSUMER)) break;
+      const uint32_t src = smem_u32(s_ring + (st.i * 2 + (block >> 2)) * C::kHalf) +
+                           (uint32_t)((block & 3) * TW_BLOCKS * p.block_bytes);
+      bool ok = true;
+#pragma unroll
+      for (int kb = 0; kb < TW_BLOCKS; ++kb) {
+        constexpr int G = 128 / GROUP;
+        const uint32_t from = src + (uint32_t)(kb * p.block_bytes);
+        const uint4 q0 = lds_v4(from + lane * 16), q1 = lds_v4(from + 512 + lane * 16);
+        const uint32_t lo[4] = {q0.x, q0.y, q0.z, q0.w}, hi[4] = {q1.x, q1.y, q1.z, q1.w};
+        uint32_t z0[G], z1[G];  // rows g and g + 8, twice each
+        if (p.has_zeros) {
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint32_t z = lds_half(from + 1024 + G * 32 + (uint32_t)((g * G + j) * 2));
+            z0[j] = __byte_perm(z, FP16 ? 0x64u : 0x43u, 0x4040);
+            z1[j] = __byte_perm(z, FP16 ? 0x64u : 0x43u, 0x4141);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < G; ++j) z0[j] = z1[j] = FP16 ? 0x64086408u : 0x43084308u;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[16];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int i = 2 * half + x;
+            const uint32_t e0 = z0[i * 32 / GROUP], e1 = z1[i * 32 / GROUP];
+            const uint32_t o0 = odd_zero<FP16>(e0), o1 = odd_zero<FP16>(e1);
+            r[8 * x] = decode_pair<FP16, 0>(lo[i], magic, e0);
+            r[8 * x + 1] = decode_pair<FP16, 0>(hi[i], magic, e1);
+            r[8 * x + 2] = decode_pair<FP16, 1>(lo[i], magic, o0);
+            r[8 * x + 3] = decode_pair<FP16, 1>(hi[i], magic, o1);
+            r[8 * x + 4] = decode_pair<FP16, 2>(lo[i], magic, e0);
+            r[8 * x + 5] = decode_pair<FP16, 2>(hi[i], magic, e1);
+            r[8 * x + 6] = decode_pair<FP16, 3>(lo[i], magic, o0);
+            r[8 * x + 7] = decode_pair<FP16, 3>(hi[i], magic, o1);
+          }
+          if (kb == 0 && half == 0) {
+            ok = wait_warp(&a_empty[ab.i], ab.ph ^ 1, abort_flag, p, ST_TIMEOUT_CONSUMER);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st_16x128b_x8(at + (uint32_t)(ab.i * C::kACols + kb * 64 + half * 32), r);
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&a_full[ab.i]);
+        mbar_arrive(&codes_empty[st.i]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ drain
+    const int set = warp / C::kDrain, quad = warp & 3, col0 = (warp % C::kDrain >> 2) * COLS;
+    const int block = 2 * quad + (lane >> 4), g = lane & 7, h = (lane >> 3) & 1;
+    const int row = quad * 32 + lane;  // of the unit's 128
+    const uint32_t at = tmem_d + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
+    Ring<C::kStages> st;
+    int it = 0;
+    bool ok = true;
+    for (int unit = first; unit < end; ++unit) {
+      float sum[COLS];
+#pragma unroll
+      for (int x = 0; x < COLS; ++x) sum[x] = 0.0f;
+      for (int c = c0; ok && c < c1; ++c, ++it, st.advance(1)) {
+        ok = wait_warp(&codes_full[st.i], st.ph, abort_flag, p, ST_TIMEOUT_EPILOGUE);
+        if (!ok) break;
+        const uint32_t scales = smem_u32(s_ring + (st.i * 2 + (block >> 2)) * C::kHalf) + 1024u +
+                                (uint32_t)((block & 3) * TW_BLOCKS * p.block_bytes + g * (128 / GROUP * 4) + h * 2);
+#pragma unroll
+        for (int x = 0; x < C::kGroups / C::kDrainSets; ++x) {
+          const int j = x * C::kDrainSets + set, d = it * C::kGroups + j, db = d % C::kDBufs;
+          const uint32_t sw = lds_half(scales + (uint32_t)(j / (128 / GROUP) * p.block_bytes + j % (128 / GROUP) * 4));
+          const float s = p.scale_fp16 ? __half2float(__ushort_as_half((uint16_t)sw)) : __uint_as_float(sw << 16);
+          ok = wait_warp(&d_full[db], (uint32_t)(d / C::kDBufs) & 1, abort_flag, p, ST_TIMEOUT_EPILOGUE);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int x0 = 0; x0 < COLS; x0 += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(at + (uint32_t)(db * T + x0), v);
+            tmem_ld_wait();
+            if (x0 + 16 == COLS) {  // this warp's last loads of the accumulator
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&d_empty[db]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[x0 + i] = fmaf(s, __uint_as_float(v[i]), sum[x0 + i]);
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&codes_empty[st.i]);
+      }
+      // The unit's sums: the second set's, the first set's added, and the outputs.
+      constexpr uint32_t kAll = C::kDrain * C::kDrainSets * 32;
+      if (C::kDrainSets > 1) {
+        if (set == 1) {
+#pragma unroll
+          for (int x = 0; x < COLS; ++x) s_out[(col0 + x) * 128 + row] = sum[x];
+        }
+        named_bar_sync(1, kAll);
+      }
+      if (set == 0) {
+#pragma unroll
+        for (int x = 0; x < COLS; ++x) {
+          float* to = &s_out[(col0 + x) * 128 + row];
+          *to = C::kDrainSets > 1 ? *to + sum[x] : sum[x];
+        }
+      }
+      if (p.cluster == 1) {
+        named_bar_sync(1, kAll);
+        const int tile = unit % p.tiles, m0 = unit / p.tiles * T, width = p.gated ? 64 : 128;
+        const int live = ok ? min(T, p.M - m0) : 0;
+        for (int x = threadIdx.x; x < live * width; x += kAll) {
+          const int m = x / width, i = x % width;
+          const int64_t n = (int64_t)tile * width + i;
+          if (n < p.N)
+            p.C[(int64_t)(m0 + m) * p.ldc + n] = to16<FP16>(
+                p.gated ? gate_of(s_out[m * 128 + i], s_out[m * 128 + 64 + i], p.act) : s_out[m * 128 + i]);
+        }
+        named_bar_sync(1, kAll);  // before the next unit's sums
+      }
+    }
+  }
+
+  __syncwarp();
+  if (p.cluster > 1) {
+    // One unit a cluster: each CTA adds and stores a share of it.
+    cluster_sync_all();
+    const int tile = first % p.tiles, m0 = first / p.tiles * T, width = p.gated ? 64 : 128;
+    const int live = first < end && !*abort_flag ? min(T, p.M - m0) : 0;
+    for (int x = rank * C::kThreads + threadIdx.x; x < live * width; x += p.cluster * C::kThreads) {
+      const int m = x / width, i = x % width;
+      const int64_t n = (int64_t)tile * width + i;
+      if (n >= p.N) continue;
+      float v[2] = {0.0f, 0.0f};
+      for (int r = 0; r < p.cluster; ++r) {
+        v[0] += __uint_as_float(ld_shared_cluster_u32(mapa_shared(smem_u32(s_out + m * 128 + i), (uint32_t)r)));
+        if (p.gated)
+          v[1] += __uint_as_float(ld_shared_cluster_u32(mapa_shared(smem_u32(s_out + m * 128 + 64 + i), (uint32_t)r)));
+      }
+      p.C[(int64_t)(m0 + m) * p.ldc + n] = to16<FP16>(p.gated ? gate_of(v[0], v[1], p.act) : v[0]);
+    }
+    cluster_sync_all();  // no CTA ends while its sums may still be read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMma0) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+template <bool FP16, int GROUP, int T>
+int tile_launch_t(const W4gTileMaps& maps, const W4gTileParams& p, int num_sms, cudaStream_t stream) {
+  using C = TileCfg<GROUP, T>;
+  auto kern = w4g_tile_kernel<FP16, GROUP, T>;
+  static std::atomic<bool> attr_set[64];
+  if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.cluster > 1 ? p.units * p.cluster : p.units < num_sms ? p.units : num_sms));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, p) != cudaSuccess) return GP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
+}
+
+template <int GROUP>
+int tile_launch_group(const W4gTileMaps& maps, const W4gTileParams& p, int rows, bool fp16, int num_sms,
+                      cudaStream_t stream) {
+  if (rows == 32)
+    return fp16 ? tile_launch_t<true, GROUP, 32>(maps, p, num_sms, stream)
+                : tile_launch_t<false, GROUP, 32>(maps, p, num_sms, stream);
+  return fp16 ? tile_launch_t<true, GROUP, 64>(maps, p, num_sms, stream)
+              : tile_launch_t<false, GROUP, 64>(maps, p, num_sms, stream);
+}
+
+}  // namespace
+
+}  // namespace gp

@@ -407,8 +407,9 @@ int gemm_unpack_w4g(const void* packed, int64_t N, int64_t K, int group, int has
  *             preceding kernel on `stream` has finished; GP_RUN_INDEPENDENT is
  *             taken as that.
  * Codes enter the products exactly; sums are fp32; one rounding at the end.
- * The weights are read once per 16 rows of A, so this is for small M; any
- * M < 2^31 is accepted.  Finite A is expected (|A| < 2^100 for bf16): rows
+ * The weights are read once per 16 rows of A, or per 32 or 64 where there are
+ * more of them and enough weights, so this is for small M; any M < 2^31 is
+ * accepted.  Finite A is expected (|A| < 2^100 for bf16): rows
  * with infinities or NaN give infinities or NaN.  Results are the same bits
  * for the same inputs.  One kernel on `stream`; nothing is allocated.
  * M == 0 or N == 0 is a no-op; K == 0 writes zeros.  Errors as
@@ -430,7 +431,7 @@ const char* gemm_status_string(int status);
  * The waits for that stage then time out after the wait limit, which
  * defaults to 2 s and is overridden by the environment variable
  * GP_WAIT_LIMIT_MS, read once per process.  The tile kernels of the gated
- * products take the armed index too.
+ * products and of the 4-bit weights take the armed index too.
  *
  * When the wait times out, the kernel drains its in-flight copies, frees
  * any tensor memory and exits.  The library's status word is set, and
