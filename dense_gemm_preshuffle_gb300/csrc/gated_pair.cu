@@ -32,6 +32,11 @@
 // INPUT, WEIGHTS): each part writes fp32 sums to the workspace and a second
 // kernel adds them in order, so results do not depend on timing.
 //
+// Measured: FORWARD 8192 x 8192 x 4096 585-624 us (0.92-0.98 of the bf16 rate),
+// the gradients of 4096 x 7168 x 4096 900-927 us in two launches (0.81-0.83);
+// the tensor cores and the power cap bound both, and a tile's start and
+// epilogue the small ones (333 x 2741 x 1093: 12.3 us, 5 of them MMAs).
+//
 // Roles as in gemm_pair.cu: warp 0 copies (lane 0 B, lane 1 A), warp 1 issues
 // the MMAs in the even CTA, warps 2-9 are the epilogue, two for each TMEM
 // lane quarter.  Every wait is bounded.

@@ -20,8 +20,13 @@
 //     group's scale and add it in fp32 registers.
 //   - Few units: a cluster of CTAs shares one unit's groups, and its sums meet
 //     through distributed shared memory in rank order.
-// Roles: drain, decode, one warp each for the MMAs, the copies of the weights
-// and of A, and A's transposition.  Every wait is bounded.
+// Roles: drain, decode, two warps that issue MMAs, one each for the copies of
+// the weights and of A, and A's transposition.  Every wait is bounded.
+// 32 x 16384 x 8192 in groups of 128: 30.5 us (0.35 of the memory's rate; two
+// passes of the streaming kernel 42.8), 64 rows 39.6.  What bounds it is the
+// hand-over among the warps: of every 256 values (of 128: 42 us), and without
+// any one of the decoding (28.4), its stores (25.8) or the transposition (28.8)
+// it is not much faster.
 #pragma once
 #include <cuda_fp16.h>
 
