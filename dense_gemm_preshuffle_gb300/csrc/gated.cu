@@ -204,8 +204,11 @@ int products_launch(const GatedArgs& a, const HostContext& ctx, const Matrix& ou
 size_t gated_workspace_bytes(int64_t M, int64_t N, int64_t K) { return (size_t)workspace_of(M, N, K).bytes; }
 
 int gated_run_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
-  if (gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)) return gated_stream_launch(a, a.H, nullptr, a.ldh, ctx, stream);
-  return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, 1, nullptr, stream);
+  switch (gated_form(a.M, a.N, a.K, ctx.num_sms)) {
+    case GATED_STREAM: return gated_stream_launch(a, a.H, nullptr, a.ldh, ctx, stream);
+    case GATED_ROWS: return gated_rows_launch(a, a.H, nullptr, a.ldh, ctx, stream);
+    default: return products_launch(a, ctx, {a.H, a.M, a.N, a.ldh}, {}, 1, nullptr, stream);
+  }
 }
 
 int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream_t stream) {
@@ -214,9 +217,10 @@ int gated_backward_launch(const GatedArgs& a, const HostContext& ctx, cudaStream
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const Matrix dg{ws, a.M, a.N, w.pitch}, du{ws + w.du, a.M, a.N, w.pitch};
   float *input_parts = reinterpret_cast<float*>(ws + w.input), *weight_parts = reinterpret_cast<float*>(ws + w.weights);
-  int rc = gated_stream_choice(a.M, a.N, a.K, ctx.num_sms)
-               ? gated_stream_launch(a, ws, ws + w.du, w.pitch, ctx, stream)
-               : products_launch(a, ctx, dg, du, w.slopes, input_parts, stream);
+  const GatedForm form = gated_form(a.M, a.N, a.K, ctx.num_sms);
+  int rc = form == GATED_STREAM ? gated_stream_launch(a, ws, ws + w.du, w.pitch, ctx, stream)
+           : form == GATED_ROWS ? gated_rows_launch(a, ws, ws + w.du, w.pitch, ctx, stream)
+                                : products_launch(a, ctx, dg, du, w.slopes, input_parts, stream);
   if (rc != GP_OK) return rc;
 
   GatedMaps maps{};

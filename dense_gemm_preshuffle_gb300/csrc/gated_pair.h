@@ -72,10 +72,23 @@ struct GatedSlopeParts {
 };
 int gated_slope_parts_launch(const GatedSlopeParts& p, int act, bool fp16, int num_sms, cudaStream_t stream);
 
-// FORWARD and SLOPES for few tokens or little work (gated_stream.cu): whether
-// it takes them, and the launch, into out0 (and out1 for SLOPES) of pitch ld.
-bool gated_stream_choice(int64_t M, int64_t N, int64_t K, int num_sms);
+// Which kernel takes FORWARD or SLOPES: the pairs' tiles, or for few tokens or
+// little work the streaming kernel (gated_stream.cu) or the weights as the
+// MMA's rows (gated_rows.cu, up to 256 tokens).
+enum GatedForm : int { GATED_TILES = 0, GATED_STREAM = 1, GATED_ROWS = 2 };
+GatedForm gated_form(int64_t M, int64_t N, int64_t K, int num_sms);
+
+// Into out0 (and out1 for SLOPES) of pitch ld.
 int gated_stream_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
                         cudaStream_t stream);
+int gated_rows_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
+                      cudaStream_t stream);
+// The latter's columns a unit, CTAs that share one, and the time of the launch
+// by its model.
+struct GatedRowsPlan {
+  int width, cluster;
+  double us;
+};
+GatedRowsPlan gated_rows_plan(int64_t M, int64_t N, int64_t K, int num_sms);
 
 }  // namespace gp

@@ -1,0 +1,417 @@
+// Gated products for tens to a few hundred tokens: the weights are the MMA's
+// rows and the tokens its columns.
+//
+//   H = act(A G^T) * (A U^T),  or  dg = dH (A U^T) act'(A G^T), du = dH act(A G^T)
+//
+// The pairs' tiles (gated_pair.cu) have 256 tokens, most of them idle here, and
+// are too few to fill the GPU with; the streaming kernel reads all of A again
+// beside every 16 rows of weights.  Here a unit is up to 64 columns of H: one
+// CTA whose MMAs (M = 128, K = 16) have those rows of G and of U, from rows 0
+// and 64 on, and N = the tokens rounded up to 16.  Fewer columns than 64 leave
+// rows of the MMA to nothing, but make as many units as there are SMs.  The reduction advances 64 values a stage of
+// a ring that TMA fills; the fp32 sums stay in tensor memory, two units' of
+// them, so that a unit's epilogue runs beside the next one's MMAs.
+// Few units: a cluster of CTAs shares one, each with a part of K, and the parts
+// meet through distributed shared memory in rank order.
+// Measured: 16 x 7168 x 4096 20.7-21.5 us (0.83 of the memory's rate; streaming
+// 24.3, pairs 25.3), 96 x 2048 x 4096 11.0 (24.6, 22.6), 128 x 4096 x 4096 16.4
+// (48.2, 23.3), 32 x 16384 x 4096 44.8 (0.90 of the memory's rate).  What an SM
+// takes in from L2 bounds it, 88 KB of weights a us, and the launch and the
+// epilogue where K is short.
+// Roles: warp 0 copies the weights, warp 1 the tokens, warp 2 issues the MMAs,
+// warps 4-11 are the epilogue, two for each TMEM lane quarter.  Every wait is
+// bounded.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gated_math.cuh"
+#include "gated_pair.h"
+#include "ptx.cuh"
+
+namespace gp {
+
+namespace {
+
+constexpr int GR_THREADS = 32 * 12;
+constexpr int GR_EPI0 = 4, GR_EPI = 8;
+constexpr int GR_WEIGHT_BYTES = 128 * 128;  // room for a stage's 64 + 64 rows of 64 values
+constexpr int GR_OUT_BYTES = 32 * 128 * 4;  // 32 tokens' sums of a unit
+constexpr int GR_MAX_STAGES = 8;
+constexpr int GR_ROOM = 232448 - GR_OUT_BYTES - 512 - 1024;
+
+struct GatedRowsMaps {
+  CUtensorMap a, g, u;
+};
+struct GatedRowsParams {
+  uint16_t *out0, *out1;  // H, or dg and du
+  int64_t ld;
+  const uint16_t* dH;
+  int64_t lddh;
+  int M, N, ksteps;
+  int tokens;  // M rounded up to 16: the MMA's columns
+  int width;   // columns of a unit, a multiple of 8 up to 64
+  int units, cluster, stages;
+  int act, fp16, b_constant;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int debug_skip_load;
+};
+
+__device__ __forceinline__ ActSlope slope_of(float v, int act) {
+  switch (act) {
+    case GP_ACT_RELU: return act_slope<GP_ACT_RELU>(v);
+    case GP_ACT_SILU: return act_slope<GP_ACT_SILU>(v);
+    default: return act_slope<GP_ACT_GELU>(v);
+  }
+}
+__device__ __forceinline__ uint16_t to_half(float v, int fp16) {
+  return (uint16_t)(fp16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
+  return v;
+}
+
+// The outputs of token m and columns n to n + 3 of H (n % 4 == 0; rows start on
+// 16-byte boundaries) from the fp32 sums g and u.
+template <bool SLOPES>
+__device__ __forceinline__ void store_outputs(const GatedRowsParams& p, int m, int64_t n, const float4& g4,
+                                              const float4& u4) {
+  const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+  const bool whole = n + 4 <= p.N;
+  uint16_t o0[4], o1[4], d16[4] = {0, 0, 0, 0};
+  if constexpr (SLOPES) {
+    const uint16_t* dh = p.dH + (int64_t)m * p.lddh + n;
+    if (whole) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(dh));
+      d16[0] = (uint16_t)w.x, d16[1] = (uint16_t)(w.x >> 16), d16[2] = (uint16_t)w.y, d16[3] = (uint16_t)(w.y >> 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) d16[e] = __ldg(dh + e);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const ActSlope s = slope_of(g[e], p.act);
+    if constexpr (SLOPES) {
+      const float d = p.fp16 ? __half2float(__ushort_as_half(d16[e])) : __uint_as_float((uint32_t)d16[e] << 16);
+      o0[e] = to_half(d * u[e] * s.slope, p.fp16);
+      o1[e] = to_half(d * s.value, p.fp16);
+    } else {
+      o0[e] = to_half(s.value * u[e], p.fp16);
+    }
+  }
+  auto put = [&](uint16_t* to, const uint16_t (&o)[4]) {
+    if (whole) {
+      *reinterpret_cast<uint2*>(to) =
+          make_uint2((uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) to[e] = o[e];
+    }
+  };
+  put(p.out0 + (int64_t)m * p.ld + n, o0);
+  if constexpr (SLOPES) put(p.out1 + (int64_t)m * p.ld + n, o1);
+}
+
+}  // namespace
+
+template <bool SLOPES>
+__global__ void __launch_bounds__(GR_THREADS, 1)
+    gated_rows_kernel(const __grid_constant__ GatedRowsMaps maps, const __grid_constant__ GatedRowsParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tok_bytes = p.tokens * 128, stage_bytes = GR_WEIGHT_BYTES + tok_bytes;
+  uint8_t* s_ring = base;  // at the end of a shared unit: its sums, [token][128]
+  float* s_out = reinterpret_cast<float*>(s_ring + p.stages * stage_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_out) + GR_OUT_BYTES);
+  uint64_t* empty = full + GR_MAX_STAGES;
+  uint64_t* accf = empty + GR_MAX_STAGES;
+  uint64_t* acce = accf + 2;
+  uint64_t* drained = acce + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], GR_EPI);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2) tmem_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // This CTA's run of units, and its part of each one's steps.
+  const int mine = (int)blockIdx.x / p.cluster, of = (int)gridDim.x / p.cluster;
+  const int first = (int)((int64_t)p.units * mine / of), end = (int)((int64_t)p.units * (mine + 1) / of);
+  const int k0 = (int)((int64_t)p.ksteps * rank / p.cluster), k1 = (int)((int64_t)p.ksteps * (rank + 1) / p.cluster);
+
+  pdl_launch_dependents();
+  if (!(warp == 0 && p.b_constant)) pdl_wait();
+
+  if (warp < 2) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int unit = first; ok && unit < end; ++unit) {
+        for (int ks = k0; ks < k1; ++ks, ++it) {
+          if (!wait_bounded(&empty[s], ph ^ 1, abort_flag, p.status, ST_TIMEOUT_PRODUCER, limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = s_ring + s * stage_bytes;
+          if (p.debug_skip_load == 1 + it) {
+            // Fault injection (host-selected): leave this stage's barrier
+            // without its arrivals, so the waits on it time out.
+          } else if (warp == 0) {
+            mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * p.width * 128));
+            tma_load_2d(dst, &maps.g, ks * 64, unit * p.width, &full[s]);
+            tma_load_2d(dst + GR_WEIGHT_BYTES / 2, &maps.u, ks * 64, unit * p.width, &full[s]);
+          } else {
+            mbar_arrive_expect_tx(&full[s], (uint32_t)tok_bytes);
+            tma_load_2d(dst + GR_WEIGHT_BYTES, &maps.a, ks * 64, 0, &full[s]);
+          }
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok || *abort_flag) {  // nothing lands after the exit
+        for (int i = 1; i <= min(it, p.stages); ++i) {
+          const int q = it - i;
+          volatile int never = 0;
+          if (p.debug_skip_load == 1 + q) continue;
+          wait_bounded(&full[q % p.stages], (uint32_t)(q / p.stages) & 1, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ MMAs
+    // The whole warp runs the loop and one lane issues: the operands' addresses
+    // stay in uniform registers, which the instructions take.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu,
+                        wait_bounded(bar, parity, abort_flag, p.status, ST_TIMEOUT_MMA, limit));
+    };
+    const uint32_t idesc = idesc_dense(p.fp16 ? 0u : 1u, p.fp16 ? 0u : 1u, 128, (uint32_t)p.tokens);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int unit = first; ok && unit < end; ++unit) {
+      const int local = unit - first, buf = local & 1;
+      ok = wait(&acce[buf], ((uint32_t)(local >> 1) & 1) ^ 1);
+      for (int ks = k0; ok && ks < k1; ++ks) {
+        ok = wait(&full[s], ph);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sw = smem_u32(s_ring + s * stage_bytes);
+        const uint64_t wdesc = smem_desc_sw128(sw), tdesc = smem_desc_sw128(sw + GR_WEIGHT_BYTES);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma<0>(tm + (uint32_t)(buf * 256), wdesc + (uint64_t)(2 * k), tdesc + (uint64_t)(2 * k), idesc,
+                    (ks > k0 || k > 0) ? 1u : 0u);
+          umma_commit(&empty[s]);
+          if (ks + 1 == k1) umma_commit(&accf[buf]);
+        }
+        __syncwarp();
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    // Every issued MMA must complete before tensor memory is released.
+    if (elect_one()) {
+      umma_commit(drained);
+      volatile int never = 0;
+      wait_bounded(drained, 0, &never, p.status, ST_TIMEOUT_DRAIN, limit);
+    }
+  } else if (warp >= GR_EPI0) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = (warp - GR_EPI0) >> 2;
+    const int row = quad * 32 + lane;  // of the MMA's: G's from 0, U's from 64 on
+    const int tid = (int)threadIdx.x - GR_EPI0 * 32;
+    bool ok = true;
+    for (int unit = first; unit < end; ++unit) {
+      const int local = unit - first, buf = local & 1;
+      if (ok) {
+        ok = wait_bounded(&accf[buf], (uint32_t)(local >> 1) & 1, abort_flag, p.status, ST_TIMEOUT_EPILOGUE, limit);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+      }
+      // 32 tokens at a time, 16 to each of a quarter's two warps.
+      for (int m0 = 0; m0 < p.tokens; m0 += 32) {
+        float* to = p.cluster > 1 ? reinterpret_cast<float*>(s_ring) + m0 * 128 : s_out;
+        const int at = m0 + half * 16;
+        if (ok && at < p.tokens) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * 256 + at), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) to[(half * 16 + x) * 128 + row] = __uint_as_float(v[x]);
+        }
+        if (m0 + 32 >= p.tokens) {  // the warp's last loads of the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce[buf]);
+        }
+        if (p.cluster == 1) {
+          named_bar_sync(1, GR_EPI * 32);
+          const int live = ok ? min(32, p.M - m0) : 0;
+          for (int x = tid; x < live * 16; x += GR_EPI * 32) {  // four columns each
+            const int i = (x & 15) * 4;
+            const int64_t n = (int64_t)unit * p.width + i;
+            const float4* sums = reinterpret_cast<const float4*>(s_out + (x >> 4) * 128 + i);
+            if (i < p.width && n < p.N) store_outputs<SLOPES>(p, m0 + (x >> 4), n, sums[0], sums[16]);
+          }
+          named_bar_sync(1, GR_EPI * 32);  // before the next 32 tokens' sums
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (p.cluster > 1) {
+    // One unit a cluster: each CTA adds and stores a share of it.
+    cluster_sync_all();
+    const int live = first < end && !*abort_flag ? p.M : 0;
+    const float* sums = reinterpret_cast<const float*>(s_ring);
+    for (int x = rank * GR_THREADS + threadIdx.x; x < live * 16; x += p.cluster * GR_THREADS) {
+      const int m = x >> 4, i = (x & 15) * 4;
+      const int64_t n = (int64_t)first * p.width + i;
+      if (i >= p.width || n >= p.N) continue;
+      const uint32_t own = smem_u32(sums + m * 128 + i);
+      float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+#pragma unroll 2
+      for (int r = 0; r < p.cluster; ++r) {
+        const uint32_t at = mapa_shared(own, (uint32_t)r);
+        const float4 gr = ld_cluster_v4(at), ur = ld_cluster_v4(at + 256);
+        g.x += gr.x, g.y += gr.y, g.z += gr.z, g.w += gr.w;
+        u.x += ur.x, u.y += ur.y, u.z += ur.z, u.w += ur.w;
+      }
+      store_outputs<SLOPES>(p, m, n, g, u);
+    }
+    cluster_sync_all();  // no CTA ends while its sums may still be read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<512>(tmem);
+  }
+}
+
+namespace {
+
+template <bool SLOPES>
+int launch_rows(const GatedRowsMaps& maps, const GatedRowsParams& p, int num_sms, cudaStream_t stream) {
+  auto kern = gated_rows_kernel<SLOPES>;
+  static std::atomic<bool> attr_set[64];
+  if (const int rc = smem_attr_once(attr_set, kern, 232448); rc != GP_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.cluster > 1 ? p.units * p.cluster : std::min(p.units, num_sms)));
+  cfg.blockDim = dim3(GR_THREADS);
+  cfg.dynamicSmemBytes = (size_t)(p.stages * (GR_WEIGHT_BYTES + p.tokens * 128) + GR_OUT_BYTES + 512 + 1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, p) != cudaSuccess) return GP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? GP_OK : GP_ERR_CUDA;
+}
+
+}  // namespace
+
+// A CTA's 64 values of K take 88 KB / us of weights and 132 of tokens, which
+// many CTAs read; a launch 4.5 us, its epilogue 0.6 and 0.4 for 64 tokens; a
+// cluster 1 us.  No plan is faster than the weights' reading.
+GatedRowsPlan gated_rows_plan(int64_t M, int64_t N, int64_t K, int num_sms) {
+  const int64_t tokens = (M + 15) / 16 * 16, ksteps = (K + 63) / 64;
+  GatedRowsPlan best{};
+  for (int width = 64; width >= 32; width -= 8) {
+    const int64_t units = (N + width - 1) / width;
+    for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
+      if (cluster > 1 && (units > clusters_at_once(cluster, num_sms) || ksteps < 8 * cluster)) break;
+      const double rounds = (double)((units * cluster + num_sms - 1) / num_sms);
+      const double steps = (double)((ksteps + cluster - 1) / cluster);
+      const double step_us = (double)width * 256.0 / 88.0e3 + (double)tokens * 128.0 / 132.0e3;
+      const double us = 4.5 + (cluster > 1 ? 1.0 : 0.0) + rounds * (steps * step_us + 0.6 + 0.4 * (double)tokens / 64.0);
+      if (best.width == 0 || us < best.us) best = {width, cluster, us};
+    }
+  }
+  best.us = std::max(best.us, 2.5 + 4.0 * (double)N * (double)K / 6.2e6);
+  return best;
+}
+
+int gated_rows_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
+                      cudaStream_t stream) {
+  GatedRowsParams p{};
+  p.out0 = static_cast<uint16_t*>(out0);
+  p.out1 = static_cast<uint16_t*>(out1);
+  p.ld = ld;
+  p.dH = static_cast<const uint16_t*>(a.dH);
+  p.lddh = a.lddh;
+  p.M = (int)a.M;
+  p.N = (int)a.N;
+  p.ksteps = (int)((a.K + 63) / 64);
+  p.tokens = (int)((a.M + 15) / 16 * 16);
+  const GatedRowsPlan plan = gated_rows_plan(a.M, a.N, a.K, ctx.num_sms);
+  p.width = plan.width;
+  p.units = (int)((a.N + plan.width - 1) / plan.width);
+  p.cluster = plan.cluster;
+  p.stages = std::min(GR_MAX_STAGES, GR_ROOM / (GR_WEIGHT_BYTES + p.tokens * 128));
+  p.act = a.act;
+  p.fp16 = a.fp16 ? 1 : 0;
+  p.b_constant = a.b_constant ? 1 : 0;
+  p.status = ctx.status;
+  p.wait_limit_ns = ctx.wait_limit_ns;
+  p.debug_skip_load = take_debug_skip_load();
+  GatedRowsMaps maps;
+  const CUtensorMapDataType type = a.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  auto rows = [&](CUtensorMap* map, const void* m, int64_t count, int64_t pitch, int box) {
+    return encode_map_2d(map, type, m, (uint64_t)a.K, (uint64_t)count, (uint64_t)pitch * 2, 64, (uint32_t)box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  int rc = rows(&maps.a, a.A, a.M, a.lda, p.tokens);
+  if (rc == GP_OK) rc = rows(&maps.g, a.G, a.N, a.ldg, p.width);
+  if (rc == GP_OK) rc = rows(&maps.u, a.U, a.N, a.ldu, p.width);
+  if (rc != GP_OK) return rc;
+  return a.dH != nullptr ? launch_rows<true>(maps, p, ctx.num_sms, stream)
+                         : launch_rows<false>(maps, p, ctx.num_sms, stream);
+}
+
+}  // namespace gp

@@ -29,6 +29,15 @@ inline int smem_attr_once(std::atomic<bool> (&done)[64], Kern kern, int bytes, i
   return GP_OK;
 }
 
+// Clusters of up to 8 CTAs, one CTA an SM, that run at once: a cluster stays
+// within one of the GPU's groups of SMs.  For 152 SMs as the occupancy query
+// answers; 16 clusters of 8 take nearly twice the time of 15.
+constexpr int kMaxCluster = 8;
+inline int64_t clusters_at_once(int cluster, int num_sms) {
+  constexpr int kOf152[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  return (int64_t)kOf152[cluster] * num_sms / 152;
+}
+
 // What a launcher needs to know of the current device (api.cu).
 struct HostContext {
   int num_sms;

@@ -22,7 +22,7 @@
 // mma.sync, not tcgen05: with 8 or 16 rows of A the arithmetic is a few percent
 // of either's rate, and register fragments spare the weights two trips through
 // shared memory.  Measured, of the memory's rate: 16-bit rows 0.95 at 1 x 8192
-// x 4096 and 0.73 at 16 x 7168 x 4096; 4-bit 0.76 at 1 x 65537 x 8192 (54.2 us),
+// x 4096; 4-bit 0.76 at 1 x 65537 x 8192 (54.2 us),
 // where integer issue bounds it: without its arithmetic it takes 41.5.
 #pragma once
 #include <cuda_bf16.h>

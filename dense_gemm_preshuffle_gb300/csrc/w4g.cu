@@ -10,7 +10,7 @@ namespace gp {
 namespace {
 
 // The tile kernel's units, and CTAs to each: a cluster where units are few and
-// every CTA keeps 16 blocks of K or more.
+// every CTA keeps 8 blocks of K or more.
 struct Tiles {
   int rows, cluster;
   int64_t across, units;
@@ -22,7 +22,8 @@ Tiles tiles_of(const W4gArgs& a, int64_t kblocks, int num_sms) {
   t.across = (a.N + width - 1) / width;
   t.units = t.across * ((a.M + t.rows - 1) / t.rows);
   t.cluster = 1;
-  while (t.cluster < 8 && t.units * t.cluster * 2 <= num_sms && kblocks >= 16 * t.cluster) t.cluster *= 2;
+  for (int c = 2; c <= kMaxCluster; ++c)
+    if (t.units <= clusters_at_once(c, num_sms) && kblocks >= 8 * c) t.cluster = c;
   return t;
 }
 

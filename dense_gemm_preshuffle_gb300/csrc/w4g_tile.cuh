@@ -125,13 +125,6 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// One lane of a converged warp, always the same.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
 // Codes 2J and 2J + 1 of a packed word, minus z, as a pair of 16-bit floats.
 // z: 128 + z as bf16; for fp16 1024 + z where J is even and -(64 + z) where it
 // is odd, which takes bits 4-7 without a shift: 1024 + 16 q, divided by 16.
