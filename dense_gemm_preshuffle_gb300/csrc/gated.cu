@@ -183,6 +183,13 @@ int products_launch(const GatedArgs& a, const HostContext& ctx, const Matrix& ou
     e.map16(&maps.c[1], out1, 32);
     e.map16(&maps.dh, {a.dH, a.M, a.N, a.lddh}, 32);
     if (parts > 1) e.parts(&maps.partial[0], partial, 2 * parts, a.M, a.N, out0.ld);
+    p.A = static_cast<const uint16_t*>(a.A);
+    p.G = static_cast<const uint16_t*>(a.G);
+    p.lda = a.lda;
+    p.ldg = a.ldg;
+    p.K = (int)a.K;
+    // one truncation of up to 2^-23 to every MMA's 16 values, half of it on average
+    p.uncertain = a.act == GP_ACT_RELU ? (float)cdiv(a.K, 16) * 0x1p-24f : 0.0f;
   }
   if (e.rc != GP_OK) return e.rc;
   const int rc = gated_pair_launch(mode, maps, p, ctx.num_sms, stream);

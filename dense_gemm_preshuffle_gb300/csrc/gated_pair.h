@@ -43,6 +43,12 @@ struct GatedPairParams {
   int fp16;
   int b_constant;
   int debug_skip_load;
+  // SLOPES with ReLU: the operands of g, and of a row's largest |g| the part
+  // below which a g's sign is not certain.
+  const uint16_t *A, *G;
+  int64_t lda, ldg;
+  int K;
+  float uncertain;
 };
 
 int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p, int num_sms, cudaStream_t stream);
