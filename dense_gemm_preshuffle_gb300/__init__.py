@@ -12,6 +12,7 @@ Build the library with ``python -c "import __graft_entry__ as g; g.build()"``
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import NamedTuple, Optional
@@ -378,6 +379,11 @@ def gated_matmul(A, W_gate, W_up, act: str = "silu", out=None, stream=None, b_co
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _backward_workspace(M: int, N: int, K: int) -> int:
+    return gemm_gated_backward_workspace_bytes(M, N, K)
+
+
 def gated_matmul_backward(A, W_gate, W_up, dH, act: str = "silu", need_dA: bool = True, need_dW: bool = True,
                           out=None, workspace=None, stream=None):
     """Gradients of sum(H * dH) for H = gated_matmul(A, W_gate, W_up, act).
@@ -394,27 +400,38 @@ def gated_matmul_backward(A, W_gate, W_up, dH, act: str = "silu", need_dA: bool 
     lda, ldg, ldu = _matrix("A", A, (M, K), t), _matrix("W_gate", W_gate, (N, K), t), _matrix("W_up", W_up, (N, K), t)
     lddh = _matrix("dH", dH, (M, N), t)
     dA, dG, dU = out if out is not None else (None, None, None)
+    ldda = lddg = lddu = (K + 7) // 8 * 8  # of the new ones
     if not need_dA:
         dA = None
     elif dA is None:
         dA = _new_rows(A, M, K)
+    else:
+        ldda = _matrix("dA", dA, (M, K), t)
     if not need_dW:
         dG = dU = None
     else:
-        dG = _new_rows(A, N, K) if dG is None else dG
-        dU = _new_rows(A, N, K) if dU is None else dU
+        if dG is None:
+            dG = _new_rows(A, N, K)
+        else:
+            lddg = _matrix("dW_gate", dG, (N, K), t)
+        if dU is None:
+            dU = _new_rows(A, N, K)
+        else:
+            lddu = _matrix("dW_up", dU, (N, K), t)
     if workspace is None:
         import torch
-        workspace = torch.empty(gemm_gated_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=A.device)
+        nbytes = _backward_workspace(M, N, K)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=A.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous CUDA tensor is wanted")
-    _check((_lib or load_library()).gemm_gated_backward(
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    code = (_lib or load_library()).gemm_gated_backward(
         A.data_ptr(), lda, W_gate.data_ptr(), ldg, W_up.data_ptr(), ldu, dH.data_ptr(), lddh, dt, M, N, K, _act(act),
-        _ptr(dA), 0 if dA is None else _matrix("dA", dA, (M, K), t),
-        _ptr(dG), 0 if dG is None else _matrix("dW_gate", dG, (N, K), t),
-        _ptr(dU), 0 if dU is None else _matrix("dW_up", dU, (N, K), t),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_for(A, stream)),
-        "gemm_gated_backward")
+        None if dA is None else dA.data_ptr(), ldda, None if dG is None else dG.data_ptr(), lddg,
+        None if dU is None else dU.data_ptr(), lddu, workspace.data_ptr(), nbytes, _stream_for(A, stream))
+    if code != GP_OK:
+        raise GemmError(code, "gemm_gated_backward")
     return dA, dG, dU
 
 

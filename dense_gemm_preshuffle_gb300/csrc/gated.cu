@@ -89,7 +89,7 @@ struct Workspace {
   int64_t part_pitch;  // of INPUT's and WEIGHTS' fp32 parts; SLOPES' have dg's
   int64_t du, input, weights, bytes;
 };
-Workspace workspace_of(int64_t M, int64_t N, int64_t K) {
+Workspace plan_workspace(int64_t M, int64_t N, int64_t K) {
   Workspace w{};
   w.parts = parts_of(M, N, K);
   w.pitch = round_up(N, 8);
@@ -100,6 +100,18 @@ Workspace workspace_of(int64_t M, int64_t N, int64_t K) {
   w.bytes = w.weights + (w.parts.weights > 1 ? 2 * w.parts.weights * N * w.part_pitch * 4 : 0);
   w.slopes = slope_parts(M, N, K);
   if (w.slopes > 1) w.bytes = std::max(w.bytes, w.input + 2 * w.slopes * M * w.pitch * 4);
+  return w;
+}
+
+// The models take a microsecond, and a call asks for the plan twice: the last
+// sizes' is kept.
+const Workspace& workspace_of(int64_t M, int64_t N, int64_t K) {
+  static thread_local int64_t sizes[3] = {-1, -1, -1};
+  static thread_local Workspace w;
+  if (sizes[0] != M || sizes[1] != N || sizes[2] != K) {
+    w = plan_workspace(M, N, K);
+    sizes[0] = M, sizes[1] = N, sizes[2] = K;
+  }
   return w;
 }
 
