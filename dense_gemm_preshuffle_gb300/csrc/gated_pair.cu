@@ -60,8 +60,8 @@ constexpr int MN_BLOCK_BYTES = 64 * 128;  // 64 values x 64 reduction steps
 template <int MODE>
 struct Cfg {
   static constexpr bool kGate = MODE != GATED_GRADIENTS;  // two products a tile
-  static constexpr int kStaging = MODE == GATED_SLOPES ? 2 : 1;  // 4 KiB staging tiles per epilogue warp
-  static constexpr int kStages = MODE == GATED_SLOPES ? 5 : 6;
+  static constexpr int kStaging = MODE == GATED_FORWARD ? 1 : 2;  // 4 KiB staging tiles per epilogue warp
+  static constexpr int kStages = MODE == GATED_FORWARD ? 6 : 5;
   static constexpr int kEpiBytes = GP_EPI_WARPS * kStaging * 4096;
   static constexpr int kSmem = kStages * STAGE_BYTES + kEpiBytes + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -99,12 +99,21 @@ __device__ __forceinline__ void slope_row(const uint32_t (&g)[32], const uint32_
   }
 }
 
-// The product of row m of A and row n of G in 64 bits, by a warp.  Products of
-// 16-bit values are exact in fp32.
+// sum += x with the rounding error kept beside it: sum + rest is exact to about
+// 48 bits.  (64-bit units are few: a warp's sum in them took 2 us.)
+__device__ __forceinline__ void add_exactly(float& sum, float& rest, float x) {
+  const float s = __fadd_rn(sum, x), b = __fsub_rn(s, sum);
+  rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(sum, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  sum = s;
+}
+
+// The product of row m of A and row n of G, by a warp.  Products of 16-bit
+// values are exact in fp32.
 __device__ __forceinline__ double exact_gate(const GatedPairParams& p, int64_t m, int64_t n, int lane) {
   const uint16_t *a = p.A + m * p.lda, *g = p.G + n * p.ldg;
   const bool fp16 = p.fp16 != 0;
-  double sum = 0.0;
+  float sum[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f};
+#pragma unroll 4
   for (int k = lane * 8; k < p.K; k += 256) {
     uint32_t aw[4] = {0u, 0u, 0u, 0u}, gw[4] = {0u, 0u, 0u, 0u};
     if (k + 8 <= p.K) {  // rows start on 16-byte boundaries
@@ -122,21 +131,24 @@ __device__ __forceinline__ double exact_gate(const GatedPairParams& p, int64_t m
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = unpack16(aw[e], fp16), y = unpack16(gw[e], fp16);
-      sum += (double)(x.x * y.x) + (double)(x.y * y.y);
+      add_exactly(sum[0], rest[0], __fmul_rn(x.x, y.x));
+      add_exactly(sum[1], rest[1], __fmul_rn(x.y, y.y));
     }
   }
+  double all = ((double)sum[0] + (double)sum[1]) + ((double)rest[0] + (double)rest[1]);
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  return sum;
+  for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+  return all;
 }
 
 // ReLU's slope jumps at 0, so a sum within its error of 0 whose sign came out
 // wrong adds or loses a whole term of every gradient in its row and column: in
 // fp16, dG of 8192 x 2880 x 4096 was off by 0.0014 of its norm (0.0004 from sums
 // in fp32 units), and is by 0.0003, its roundings.  Such sums, some seven in
-// 10^5, are taken again in 64 bits: at most two in a warp's 32 x 32 sums, so that
-// inputs with structure cannot make many.  Sums that are 0 stay.  It costs
-// nothing that a timing shows (4096 x 7168 x 4096: 899 us, SiLU 900).
+// 10^5, are taken again with their roundings kept: at most two in a warp's 32 x
+// 32 sums, so that inputs with structure cannot make many.  Sums that are 0
+// stay.  The backward pass of 1001 x 1397 x 2051 takes 4 us more for it (51.5
+// against 47.2), of 2048 x 4096 x 4096 3%.
 __device__ __forceinline__ void settle_signs(uint32_t (&g)[32], const GatedPairParams& p, const GatedProduct& of,
                                              int row0, int n0, int lane) {
   float top = 0.0f;
@@ -238,7 +250,10 @@ __device__ __forceinline__ bool tile_of(int i, int pair, int pairs, const GatedP
   return true;
 }
 
-template <int MODE>
+// SETTLE: SLOPES with ReLU, whose uncertain signs are settled.  A kernel of its
+// own: in one with the other activations it cost SiLU 5 us of 48 (1001 x 1397 x
+// 2051) without being run.
+template <int MODE, bool SETTLE>
 __global__ void __launch_bounds__(GP_THREADS, 1)
     gated_pair_kernel(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedPairParams p) {
   using C = Cfg<MODE>;
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     const int quad = warp & 3;         // TMEM lanes this warp may access: quad*32 .. +31
     const int chalf = (warp - 2) / 4;  // this warp takes the 64-column chunks c with c % 2 == chalf
     uint8_t* stg = s_epi + (warp - 2) * (C::kStaging * 4096);
-    uint8_t* stg2 = stg + 4096;  // SLOPES
+    uint8_t* stg2 = stg + 4096;
     const uint32_t stg_row = smem_u32(stg) + lane * 128;
     const uint32_t acce_leader = mapa_shared(smem_u32(acce), 0);
     const bool fp16 = p.fp16 != 0;
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             continue;
           }
           if constexpr (MODE == GATED_SLOPES) {
-            if (p.uncertain > 0.0f) settle_signs(gr, p, g, row0, n0 + h * 32, lane);
+            if constexpr (SETTLE) settle_signs(gr, p, g, row0, n0 + h * 32, lane);
             uint32_t d[16], dg[16], du[16];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -536,15 +551,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
           bulk_commit_group();
         }
       } else {
+        // Two staging tiles in turn; every one closes a bulk group, an empty one
+        // if it is not stored, so that all but the last have been read.
         const int out = a.product + a.out;  // dA, dG, dU
 #pragma unroll 1
         for (int c = chalf; c < 4; c += 2) {
           const int n0 = a.nb * 256 + c * 64;
-          const bool inside = row0 < g.rows && n0 < g.tail;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r[32];
             tmem_ld_32x32b_x32(tbase + (uint32_t)(c * 64 + h * 32), r);
+            if (h == 0 || g.parts > 1) {
+              if (lane == 0) bulk_wait_group_read<1>();
+              __syncwarp();
+            }
             tmem_ld_wait();
             if (c + 2 >= 4 && h == 1) {  // this warp's last loads of the accumulator: free it
               tc_fence_before();
@@ -553,35 +573,31 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             }
             if (g.parts > 1) {
               // fp32 sums of this part: a 32 x 32 tile, 128 bytes a row
-              if (lane == 0) bulk_wait_group_read<0>();
-              __syncwarp();
-              stage_fp32(stg_row, lane, r);
+              uint8_t* to = h == 0 ? stg : stg2;
+              stage_fp32(stg_row + (uint32_t)(h * 4096), lane, r);
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0 && row0 < g.rows && n0 + h * 32 < g.cols) {
-                tma_store_3d(&maps.partial[a.product], n0 + h * 32, row0, a.out * g.parts + a.part, stg);
+              if (lane == 0) {
+                if (row0 < g.rows && n0 + h * 32 < g.cols)
+                  tma_store_3d(&maps.partial[a.product], n0 + h * 32, row0, a.out * g.parts + a.part, to);
                 bulk_commit_group();
               }
             } else {
-              if (h == 0) {
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-              }
               uint32_t pk[16];
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 const float lo = __uint_as_float(r[2 * q]), hi = __uint_as_float(r[2 * q + 1]);
                 pk[q] = fp16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
               }
-              stage_row(stg_row, lane, h, pk);
+              stage_row(stg_row + (uint32_t)((c >> 1) * 4096), lane, h, pk);
               store_tail(p, g, out, row0 + lane, n0 + h * 32, pk);
             }
           }
           if (g.parts == 1) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && inside) {
-              tma_store_2d(&maps.c[out], n0, row0, stg);
+            if (lane == 0) {
+              if (row0 < g.rows && n0 < g.tail) tma_store_2d(&maps.c[out], n0, row0, c >> 1 ? stg2 : stg);
               bulk_commit_group();
             }
           }
@@ -669,10 +685,10 @@ __global__ void __launch_bounds__(256) gated_slope_parts_kernel(const __grid_con
   }
 }
 
-template <int MODE>
+template <int MODE, bool SETTLE = false>
 int launch_mode(const GatedMaps& maps, GatedPairParams p, int num_sms, cudaStream_t stream) {
   using C = Cfg<MODE>;
-  auto kern = gated_pair_kernel<MODE>;
+  auto kern = gated_pair_kernel<MODE, SETTLE>;
   static std::atomic<bool> attr_set[64];
   if (const int rc = smem_attr_once(attr_set, kern, C::kSmem); rc != GP_OK) return rc;
   const int pairs = num_sms / 2;
@@ -700,7 +716,9 @@ int launch_mode(const GatedMaps& maps, GatedPairParams p, int num_sms, cudaStrea
 int gated_pair_launch(int mode, const GatedMaps& maps, const GatedPairParams& p, int num_sms, cudaStream_t stream) {
   switch (mode) {
     case GATED_FORWARD: return launch_mode<GATED_FORWARD>(maps, p, num_sms, stream);
-    case GATED_SLOPES: return launch_mode<GATED_SLOPES>(maps, p, num_sms, stream);
+    case GATED_SLOPES:
+      return p.act == GP_ACT_RELU ? launch_mode<GATED_SLOPES, true>(maps, p, num_sms, stream)
+                                  : launch_mode<GATED_SLOPES>(maps, p, num_sms, stream);
     default: return launch_mode<GATED_GRADIENTS>(maps, p, num_sms, stream);
   }
 }
