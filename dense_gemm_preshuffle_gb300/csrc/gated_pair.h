@@ -80,7 +80,8 @@ int gated_slope_parts_launch(const GatedSlopeParts& p, int act, bool fp16, int n
 
 // Which kernel takes FORWARD or SLOPES: the pairs' tiles, or for few tokens or
 // little work the streaming kernel (gated_stream.cu) or the weights as the
-// MMA's rows (gated_rows.cu, up to 256 tokens).
+// MMA's rows (gated_rows.cu, up to kRowsTokens tokens).
+constexpr int64_t kRowsTokens = 1024;
 enum GatedForm : int { GATED_TILES = 0, GATED_STREAM = 1, GATED_ROWS = 2 };
 GatedForm gated_form(int64_t M, int64_t N, int64_t K, int num_sms);
 
@@ -89,10 +90,10 @@ int gated_stream_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, 
                         cudaStream_t stream);
 int gated_rows_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, const HostContext& ctx,
                       cudaStream_t stream);
-// The latter's columns a unit, CTAs that share one, and the time of the launch
-// by its model.
+// The latter's tokens and columns a unit, CTAs that share one, and the time of
+// the launch by its model.
 struct GatedRowsPlan {
-  int width, cluster;
+  int tokens, width, cluster;
   double us;
 };
 GatedRowsPlan gated_rows_plan(int64_t M, int64_t N, int64_t K, int num_sms);

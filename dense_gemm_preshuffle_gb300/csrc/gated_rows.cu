@@ -1,5 +1,5 @@
-// Gated products for tens to a few hundred tokens: the weights are the MMA's
-// rows and the tokens its columns.
+// Gated products for tens to some hundreds of tokens: the weights are the MMA's
+// rows and the tokens its columns, up to 256 of them a unit.
 //
 //   H = act(A G^T) * (A U^T),  or  dg = dH (A U^T) act'(A G^T), du = dH act(A G^T)
 //
@@ -49,8 +49,9 @@ struct GatedRowsParams {
   const uint16_t* dH;
   int64_t lddh;
   int M, N, ksteps;
-  int tokens;  // M rounded up to 16: the MMA's columns
-  int width;   // columns of a unit, a multiple of 8 up to 64
+  int tokens;  // of a unit, the MMA's columns: a multiple of 16 up to 256
+  int width;   // columns of H of a unit, a multiple of 8 up to 64
+  int tiles;   // across H; a unit is one of them with `tokens` tokens
   int units, cluster, stages;
   int act, fp16, b_constant;
   uint32_t* status;
@@ -190,11 +191,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
             // without its arrivals, so the waits on it time out.
           } else if (warp == 0) {
             mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * p.width * 128));
-            tma_load_2d(dst, &maps.g, ks * 64, unit * p.width, &full[s]);
-            tma_load_2d(dst + GR_WEIGHT_BYTES / 2, &maps.u, ks * 64, unit * p.width, &full[s]);
+            tma_load_2d(dst, &maps.g, ks * 64, unit % p.tiles * p.width, &full[s]);
+            tma_load_2d(dst + GR_WEIGHT_BYTES / 2, &maps.u, ks * 64, unit % p.tiles * p.width, &full[s]);
           } else {
             mbar_arrive_expect_tx(&full[s], (uint32_t)tok_bytes);
-            tma_load_2d(dst + GR_WEIGHT_BYTES, &maps.a, ks * 64, 0, &full[s]);
+            tma_load_2d(dst + GR_WEIGHT_BYTES, &maps.a, ks * 64, unit / p.tiles * p.tokens, &full[s]);
           }
           if (++s == p.stages) {
             s = 0;
@@ -285,12 +286,13 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
         }
         if (p.cluster == 1) {
           named_bar_sync(1, GR_EPI * 32);
-          const int live = ok ? min(32, p.M - m0) : 0;
+          const int token0 = unit / p.tiles * p.tokens;
+          const int live = ok ? min(32, min(p.tokens, p.M - token0) - m0) : 0;
           for (int x = tid; x < live * 16; x += GR_EPI * 32) {  // four columns each
             const int i = (x & 15) * 4;
-            const int64_t n = (int64_t)unit * p.width + i;
+            const int64_t n = (int64_t)(unit % p.tiles) * p.width + i;
             const float4* sums = reinterpret_cast<const float4*>(s_out + (x >> 4) * 128 + i);
-            if (i < p.width && n < p.N) store_outputs<SLOPES>(p, m0 + (x >> 4), n, sums[0], sums[16]);
+            if (i < p.width && n < p.N) store_outputs<SLOPES>(p, token0 + m0 + (x >> 4), n, sums[0], sums[16]);
           }
           named_bar_sync(1, GR_EPI * 32);  // before the next 32 tokens' sums
         }
@@ -302,11 +304,12 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
   if (p.cluster > 1) {
     // One unit a cluster: each CTA adds and stores a share of it.
     cluster_sync_all();
-    const int live = first < end && !*abort_flag ? p.M : 0;
+    const int token0 = first / p.tiles * p.tokens;
+    const int live = first < end && !*abort_flag ? min(p.tokens, p.M - token0) : 0;
     const float* sums = reinterpret_cast<const float*>(s_ring);
     for (int x = rank * GR_THREADS + threadIdx.x; x < live * 16; x += p.cluster * GR_THREADS) {
       const int m = x >> 4, i = (x & 15) * 4;
-      const int64_t n = (int64_t)first * p.width + i;
+      const int64_t n = (int64_t)(first % p.tiles) * p.width + i;
       if (i >= p.width || n >= p.N) continue;
       const uint32_t own = smem_u32(sums + m * 128 + i);
       float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
         g.x += gr.x, g.y += gr.y, g.z += gr.z, g.w += gr.w;
         u.x += ur.x, u.y += ur.y, u.z += ur.z, u.w += ur.w;
       }
-      store_outputs<SLOPES>(p, m, n, g, u);
+      store_outputs<SLOPES>(p, token0 + m, n, g, u);
     }
     cluster_sync_all();  // no CTA ends while its sums may still be read
   }
@@ -360,17 +363,17 @@ int launch_rows(const GatedRowsMaps& maps, const GatedRowsParams& p, int num_sms
 // many CTAs read; a launch 4.5 us, its epilogue 0.6 and 0.4 for 64 tokens; a
 // cluster 1 us.  No plan is faster than the weights' reading.
 GatedRowsPlan gated_rows_plan(int64_t M, int64_t N, int64_t K, int num_sms) {
-  const int64_t tokens = (M + 15) / 16 * 16, ksteps = (K + 63) / 64;
+  const int64_t chunks = (M + 255) / 256, tokens = ((M + chunks - 1) / chunks + 15) / 16 * 16, ksteps = (K + 63) / 64;
   GatedRowsPlan best{};
   for (int width = 64; width >= 32; width -= 8) {
-    const int64_t units = (N + width - 1) / width;
+    const int64_t units = (N + width - 1) / width * chunks;
     for (int cluster = 1; cluster <= kMaxCluster; ++cluster) {
       if (cluster > 1 && (units > clusters_at_once(cluster, num_sms) || ksteps < 8 * cluster)) break;
       const double rounds = (double)((units * cluster + num_sms - 1) / num_sms);
       const double steps = (double)((ksteps + cluster - 1) / cluster);
       const double step_us = (double)width * 256.0 / 88.0e3 + (double)tokens * 128.0 / 132.0e3;
       const double us = 4.5 + (cluster > 1 ? 1.0 : 0.0) + rounds * (steps * step_us + 0.6 + 0.4 * (double)tokens / 64.0);
-      if (best.width == 0 || us < best.us) best = {width, cluster, us};
+      if (best.width == 0 || us < best.us) best = {(int)tokens, width, cluster, us};
     }
   }
   best.us = std::max(best.us, 2.5 + 4.0 * (double)N * (double)K / 6.2e6);
@@ -388,10 +391,13 @@ int gated_rows_launch(const GatedArgs& a, void* out0, void* out1, int64_t ld, co
   p.M = (int)a.M;
   p.N = (int)a.N;
   p.ksteps = (int)((a.K + 63) / 64);
-  p.tokens = (int)((a.M + 15) / 16 * 16);
   const GatedRowsPlan plan = gated_rows_plan(a.M, a.N, a.K, ctx.num_sms);
+  p.tokens = plan.tokens;
   p.width = plan.width;
-  p.units = (int)((a.N + plan.width - 1) / plan.width);
+  p.tiles = (int)((a.N + plan.width - 1) / plan.width);
+  const int64_t units = p.tiles * ((a.M + plan.tokens - 1) / plan.tokens);
+  if (units * (p.ksteps + 1) > 0x7FFFFFFF) return GP_ERR_SHAPE;  // steps are counted in 32 bits
+  p.units = (int)units;
   p.cluster = plan.cluster;
   p.stages = std::min(GR_MAX_STAGES, GR_ROOM / (GR_WEIGHT_BYTES + p.tokens * 128));
   p.act = a.act;

@@ -46,7 +46,7 @@ GatedForm gated_form(int64_t M, int64_t N, int64_t K, int num_sms) {
     const char* e = std::getenv("GP_GATED_STREAM");
     return (e == nullptr || *e == '\0') ? -1 : std::atoi(e);
   }();
-  if (forced >= 0) return forced == 1 ? GATED_STREAM : forced == 2 && M <= 256 ? GATED_ROWS : GATED_TILES;
+  if (forced >= 0) return forced == 1 ? GATED_STREAM : forced == 2 && M <= kRowsTokens ? GATED_ROWS : GATED_TILES;
   // Microseconds of each form by its measured rates, and the smaller.
   // Streaming: a unit reads 16 rows of G and of U; the rate of a block falls
   // with the rows of A beside them, and is higher where it has an SM alone, or
@@ -64,7 +64,7 @@ GatedForm gated_form(int64_t M, int64_t N, int64_t K, int num_sms) {
   const double waves = (double)((tiles + pairs - 1) / pairs);
   const double tile_us = std::max(4.5 + waves * 0.285 * (double)((K + 63) / 64), 6.0 + 4e-6 * (double)N * (double)K / 6.0);
   // Weights as the MMA's rows, from more tokens than the streaming MMA's 8 columns.
-  if (M > 8 && M <= 256 && gated_rows_plan(M, N, K, num_sms).us < std::min(stream_us, tile_us)) return GATED_ROWS;
+  if (M > 8 && M <= kRowsTokens && gated_rows_plan(M, N, K, num_sms).us < std::min(stream_us, tile_us)) return GATED_ROWS;
   return stream_us < tile_us ? GATED_STREAM : GATED_TILES;
 }
 

@@ -141,3 +141,17 @@ def test_timeout_is_reported_and_the_context_survives(M, N, K, b_constant):
     """A stage's copies left out, as the bounded waits of the other kernels are tested."""
     sizes = f"M, N, K, b_constant = {M}, {N}, {K}, {b_constant}\n"
     assert "next calls ok" in child(sizes + FAULT, GP_GATED_STREAM="2", GP_WAIT_LIMIT_MS="200")
+
+
+CHUNKS = HEAD + textwrap.dedent("""
+    for i, (M, N, K) in enumerate([(257, 500, 4097), (300, 1000, 2000), (513, 90, 1500), (700, 831, 130),
+                                   (1024, 250, 640), (1001, 3000, 65)]):
+        t.check(M, N, K, ("bf16", "fp16")[i % 2], ("silu", "gelu", "relu")[i % 3], seed=i)
+    assert gp.gemm_last_device_status() == 0
+    print("all shapes right")
+""")
+
+
+@pytest.mark.parametrize("form", ["2", ""])
+def test_more_tokens_than_one_unit_takes(form):
+    assert "all shapes right" in child(CHUNKS, GP_GATED_STREAM=form)
