@@ -60,7 +60,6 @@ int tile_launch(const W4gArgs& a, const W4gLayout& l, const HostContext& ctx, cu
   p.kblocks = (int)l.kblocks;
   p.M = (int)a.M;
   p.N = (int)a.N;
-  p.K = (int)a.K;
   p.gated = a.U != nullptr ? 1 : 0;
   const Tiles t = tiles_of(a, l.kblocks, ctx.num_sms);
   // more outputs than the memory holds; and steps are counted in 32 bits

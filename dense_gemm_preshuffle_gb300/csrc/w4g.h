@@ -14,7 +14,7 @@ struct W4gTileParams {
   uint16_t* C;
   int64_t ldc;
   int block_bytes, kblocks;  // of the packed matrices
-  int M, N, K;
+  int M, N;
   int tiles, units;  // units: tiles * chunks of rows of A
   int cluster;       // CTAs that share a unit
   int gated, act, has_zeros, scale_fp16, b_constant;

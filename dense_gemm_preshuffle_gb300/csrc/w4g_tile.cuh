@@ -13,7 +13,7 @@
 //     low bits of 128's (bf16) or 1024's (fp16) fraction.
 //   - A's rows are the MMA's T columns, by TMA.  In a packed word four lanes
 //     hold 8 consecutive values each where the fragments have pairs in turn,
-//     so two warps transpose the 4 x 4 words of every 64 bytes of A in place;
+//     so a few warps transpose the 4 x 4 words of every 64 bytes of A in place;
 //     the sum does not change when both operands are permuted alike.
 //   - Every group is an accumulator of its own (a ring of them in tensor
 //     memory).  The drain warps, a weight row to a thread, multiply it by the
@@ -24,8 +24,8 @@
 // the weights and of A, and A's transposition.  Every wait is bounded.
 // 32 x 16384 x 8192 in groups of 128: 30.5 us (0.35 of the memory's rate; two
 // passes of the streaming kernel 42.8), 64 rows 39.6.  What bounds it is the
-// hand-over among the warps: of every 256 values (of 128: 42 us), and without
-// any one of the decoding (28.4), its stores (25.8) or the transposition (28.8)
+// hand-over among the warps, of every 256 values (of every 128 to the MMAs alone
+// it takes 31.5, of every 128 throughout 42 and more), and without any one of the decoding (28.4), its stores (25.8) or the transposition (28.8)
 // it is not much faster.
 #pragma once
 #include <cuda_fp16.h>

@@ -309,8 +309,9 @@ typedef enum gp_act {
  * size is negative or >= 2^31, a matrix has more than 2^50 elements, or a
  * pitch is shorter than its row or not a multiple of 8), GP_ERR_ALIGNMENT (a
  * pointer is not 16-byte aligned).
- * Which of two kernels runs, the one on tensor-core tiles or the one that
- * streams the weights past few tokens, follows from the sizes alone.
+ * Which of three kernels runs (tensor-core tiles of many tokens, of tens to
+ * hundreds, or the one that streams the weights past few) follows from the
+ * sizes alone.
  */
 int gemm_gated_run(const void* A, int64_t lda, const void* G, int64_t ldg, const void* U, int64_t ldu, int dtype,
                    int64_t M, int64_t N, int64_t K, int act, void* H, int64_t ldh, unsigned flags, void* stream);
