@@ -25,8 +25,8 @@
 // 32 x 16384 x 8192 in groups of 128: 30.5 us (0.35 of the memory's rate; two
 // passes of the streaming kernel 42.8), 64 rows 39.6.  What bounds it is the
 // hand-over among the warps, of every 256 values (of every 128 to the MMAs alone
-// it takes 31.5, of every 128 throughout 42 and more), and without any one of the decoding (28.4), its stores (25.8) or the transposition (28.8)
-// it is not much faster.
+// it takes 31.5, of every 128 throughout 42 and more): without the decoding it
+// takes 28.4, without its stores 25.8, without the transposition 28.8.
 #pragma once
 #include <cuda_fp16.h>
 
